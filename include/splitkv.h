@@ -24,6 +24,11 @@
  *                       batch_pod.cu: prefill and decode work fused in one kernel).
  *   skv_causal_tables   Host planner that turns causal / multi-token attention into a prefix
  *                       call, a diagonal call over token rows and an exact merge.
+ *   skv_rope_apply      Rotary positions of queries and keys (both pair layouts, part of the head,
+ *                       frequencies stretched for long contexts by skv_rope_frequencies).
+ *   skv_paged_kv_append New keys and values into the paged cache, rotated on the way; the cache
+ *                       is bf16, e4m3 with one scale, or e4m3 / int8 with a scale for each block
+ *                       of tokens and head.
  *   skv_mla_splice      The fetch primitive's local compute: move a chunk's latent rows between
  *                       page lists and re-rotate their RoPE part to the new positions ("Move
  *                       the Query, Not the Cache", problem statement and Methodology: fetch
@@ -83,7 +88,7 @@ typedef enum {
 #define SKV_DEV_PAGE_OOB 17  /* a page id outside [0, num_pages)                              */
 #define SKV_DEV_PLAN_BAD 18  /* a work item outside the request's pages / query rows          */
 
-typedef enum { SKV_BF16 = 0, SKV_F32 = 1, SKV_E4M3 = 2 } skv_dtype;
+typedef enum { SKV_BF16 = 0, SKV_F32 = 1, SKV_E4M3 = 2, SKV_I8 = 3 } skv_dtype;
 
 /* split policies for the planners */
 typedef enum {
@@ -412,6 +417,130 @@ typedef struct {
 
 SKV_API skv_status skv_mla_splice(const skv_splice_params* p, const skv_splice_chunk* chunks_h,
                                   int32_t num_chunks, skv_stream_t stream);
+
+/* -------------------------------------------------------------------------------------------
+ * Rotary positions.  Pair p of a head's first `dim` values turns by the angle
+ *   position * inv_freq[p]:  a' = m (a cos - b sin), b' = m (a sin + b cos), m = mscale.
+ *   Pairs are (2p, 2p+1) for SKV_ROPE_INTERLEAVED and (p, p + dim/2) for SKV_ROPE_HALVES; values
+ *   from `dim` on are copied.  The angle is formed as an exact integer multiple of the frequency
+ *   held in 2^-64 turns, so it is as good at position 2^30 as at 1; rotation in fp32, one rounding
+ *   to the output type.
+ * ----------------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t dim;              /* rotated values of a head: a multiple of 16 in [0, min(256, head_dim)] */
+  int32_t layout;           /* SKV_ROPE_INTERLEAVED or SKV_ROPE_HALVES                         */
+  double theta;             /* inv_freq[p] = theta^(-2p/dim) when inv_freq_h is NULL (>= 1)      */
+  const double* inv_freq_h; /* optional HOST [dim/2] frequencies in radians per position, read  */
+                            /*   before the call returns (|w| < 2^32)                           */
+  float mscale;             /* factor on cos and sin (finite, > 0; 1 = none)                    */
+} skv_rope;
+
+/* ways skv_rope_frequencies stretches the frequencies f_p = theta^(-2p/dim) for long contexts */
+typedef enum {
+  SKV_ROPE_SCALE_NONE = 0,
+  SKV_ROPE_SCALE_LINEAR = 1, /* f / factor (position interpolation)                            */
+  SKV_ROPE_SCALE_NTK = 2,    /* theta * factor^(dim/(dim-2)) as the base                        */
+  SKV_ROPE_SCALE_YARN = 3,   /* f / factor for pairs that turn fewer than `low` times in          */
+                             /*   original_context positions, f for those that turn more than     */
+                             /*   `high` times, a linear ramp over the pairs between (its ends      */
+                             /*   floored / ceiled); mscale = 0.1 ln(factor) + 1                  */
+  SKV_ROPE_SCALE_BANDS = 4   /* as YARN with the ramp linear in the number of turns and no mscale  */
+} skv_rope_scaling;
+
+/* Host helper: fills inv_freq_h [dim/2] and *mscale (either may be NULL).  dim even >= 2, theta > 1,
+ * factor >= 1; original_context > 0 and 0 < low < high for YARN and BANDS (usual: 1 and 32 for YARN,
+ * 1 and 4 for BANDS); NTK needs dim > 2. */
+SKV_API skv_status skv_rope_frequencies(int32_t dim, double theta, int32_t scaling, double factor,
+                                        double original_context, double low, double high, double* inv_freq_h,
+                                        float* mscale);
+
+/* Arguments of skv_rope_apply.  x(token, head, d) = x[token*stride[0] + head*stride[1] + d]. */
+typedef struct {
+  const void* q;            /* [num_tokens, num_q_heads, head_dim] of dtype (num_q_heads 0: unused) */
+  void* q_out;              /* may be q itself with the same strides (in place), else disjoint    */
+  const void* k;            /* [num_tokens, num_k_heads, head_dim] (num_k_heads 0: unused)         */
+  void* k_out;
+  int64_t q_stride[2];      /* (token, head) strides in elements, multiples of 16 bytes           */
+  int64_t q_out_stride[2];
+  int64_t k_stride[2];
+  int64_t k_out_stride[2];
+  const int32_t* positions; /* [num_tokens], any int32 value                                      */
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_k_heads;
+  int32_t head_dim;         /* a multiple of 8, <= 1024                                            */
+  int32_t dtype;            /* SKV_BF16 or SKV_F32                                                 */
+  int32_t inverse;          /* nonzero: turn by -position (undoes the rotation when mscale is 1;     */
+                            /*   always the rotation's transpose, which takes gradients back)       */
+  skv_rope rope;
+} skv_rope_params;
+
+SKV_API skv_status skv_rope_apply(const skv_rope_params* p, skv_stream_t stream);
+
+/* -------------------------------------------------------------------------------------------
+ * skv_paged_kv_append -- writes new tokens' keys and values into the paged cache.
+ *   The tokens of request r are rows append_indptr[r] .. append_indptr[r+1] of k and v; the page
+ *   table describes the requests AFTER the append, so new token i of n takes position
+ *   L_r - n + i and its slot.  Keys (and q, when given) turn by `rope` at that position, or at
+ *   positions[row] when given.  Rows of k / v / q from append_indptr[batch] on are not read, and
+ *   q_out rows there are left as they are: a batch padded to num_rows rows replays one graph
+ *   while lengths change on the device.
+ *
+ *   Cache types: SKV_BF16; SKV_E4M3 with the per-tensor kv_scale (block_tokens 0): code =
+ *   rn(x / kv_scale), saturating at 448; SKV_E4M3 or SKV_I8 with block scales (block_tokens > 0, a
+ *   divisor of page_size): slots [b*block_tokens, (b+1)*block_tokens) of a page share one fp32
+ *   scale for each head, k_scale(page, b, head) = k_scale[page*s[0] + b*s[1] + head*s[2]] (any
+ *   strides), value = scale * code.  Appending to a block sets
+ *     scale' = max(scale, amax / qmax)   qmax = 448 (e4m3) or 127 (int8, codes in [-127, 127]),
+ *   amax over the new rows of the head in the block.  When the block's first slot is among the new
+ *   ones, its old scale counts as 0 and its other codes stay as they are; otherwise, where the
+ *   scale grew, the codes of the block's other slots are written again as
+ *   rn(code * scale / scale'), so that they keep their values.  A block whose scale' is below
+ *   2^-126 gets scale 0 and new codes of zero.  A value that is not finite spoils at most its own block
+ *   and head.
+ *
+ *   No page slot, and with block scales no block, may be written by two requests of a call; the
+ *   cache, scales and outputs must not overlap the inputs.  Errors found on the device (a page
+ *   id outside [0, num_pages): SKV_DEV_PAGE_OOB; a request shorter than its new tokens:
+ *   SKV_DEV_PLAN_BAD) go to *status and skip the tokens concerned.
+ * ----------------------------------------------------------------------------------------- */
+typedef struct {
+  const void* k;            /* bf16 [num_rows, Hk, D], (token, head) strides                        */
+  const void* v;
+  int64_t k_row_stride[2];  /* elements, multiples of 8                                            */
+  int64_t v_row_stride[2];
+  void* k_cache;            /* cache and its (page, slot, head) strides as in skv_paged_params       */
+  void* v_cache;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int32_t kv_dtype;         /* SKV_BF16, SKV_E4M3 or SKV_I8                                        */
+  float kv_scale;           /* SKV_E4M3 without block scales (finite, > 0)                           */
+  int32_t block_tokens;     /* tokens that share a scale; 0: none (SKV_I8 needs > 0); <= 256         */
+  float* k_scale;
+  float* v_scale;
+  int64_t k_scale_stride[3];
+  int64_t v_scale_stride[3];
+  const int32_t* append_indptr; /* [batch+1], append_indptr[0] = 0                                */
+  const int32_t* kv_indptr; /* page table after the append                                         */
+  const int32_t* kv_indices;
+  const int32_t* kv_last_page_len;
+  const int32_t* positions; /* optional [num_rows] rotation positions                               */
+  int32_t batch;
+  int32_t num_rows;         /* rows of k and v (>= append_indptr[batch])                            */
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;         /* 64 or 128                                                            */
+  skv_rope rope;            /* dim 0: no rotation                                                    */
+  const void* q;            /* optional bf16 [num_rows, num_q_heads, D] turned into q_out            */
+  void* q_out;              /* may be q itself with the same strides                                */
+  int64_t q_stride[2];
+  int64_t q_out_stride[2];
+  int32_t num_q_heads;      /* 0: no q                                                              */
+  int32_t* status;
+} skv_append_params;
+
+SKV_API skv_status skv_paged_kv_append(const skv_append_params* p, skv_stream_t stream);
 
 /* -------------------------------------------------------------------------------------------
  * skv_paged_kv_gather -- test hook for the page-table walk: copies the logical K and V of every

@@ -7,7 +7,8 @@ there is no fallback path.
 
 Functions mirror the C ABI in include/splitkv.h:
 ``plan_paged``, ``paged_attn_fwd``, ``pod_attn_fwd``, ``plan_mla``, ``mla_decode_fwd``, ``merge_states``,
-``paged_kv_gather``, ``mla_splice``, ``mla_fold_ratio``, ``status_str``, ``version``.
+``paged_kv_gather``, ``mla_splice``, ``rope_frequencies``, ``rope_apply``, ``paged_kv_append``,
+``mla_fold_ratio``, ``status_str``, ``version``.
 """
 from __future__ import annotations
 
@@ -26,9 +27,10 @@ _lib = ctypes.CDLL(_LIB_PATH)
 # ----------------------------------------------------------------------------- constants
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_WORKSPACE, ERR_CUDA = range(6)
 DEV_OK, DEV_TIMEOUT, DEV_PAGE_OOB, DEV_PLAN_BAD = 0, 16, 17, 18
-BF16, F32, E4M3 = 0, 1, 2
+BF16, F32, E4M3, I8 = 0, 1, 2, 3
 ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
 _ROPE = {"interleaved": ROPE_INTERLEAVED, "halves": ROPE_HALVES}
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 SPLIT_NONE, SPLIT_FIXED, SPLIT_BALANCED, SPLIT_EXPLICIT = 0, 1, 2, 3
 _POLICY = {"none": SPLIT_NONE, "fixed": SPLIT_FIXED, "balanced": SPLIT_BALANCED, "explicit": SPLIT_EXPLICIT}
 
@@ -85,6 +87,33 @@ class SpliceChunk(ctypes.Structure):
                 ("delta_pos", ctypes.c_int64)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("theta", ctypes.c_double),
+                ("inv_freq_h", _vp), ("mscale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("q_out", _vp), ("k", _vp), ("k_out", _vp),
+                ("q_stride", ctypes.c_int64 * 2), ("q_out_stride", ctypes.c_int64 * 2),
+                ("k_stride", ctypes.c_int64 * 2), ("k_out_stride", ctypes.c_int64 * 2),
+                ("positions", _vp), ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("rope", Rope)]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_row_stride", ctypes.c_int64 * 2), ("v_row_stride", ctypes.c_int64 * 2),
+                ("k_cache", _vp), ("v_cache", _vp), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3),
+                ("kv_dtype", ctypes.c_int32), ("kv_scale", ctypes.c_float), ("block_tokens", ctypes.c_int32),
+                ("k_scale", _vp), ("v_scale", _vp), ("k_scale_stride", ctypes.c_int64 * 3),
+                ("v_scale_stride", ctypes.c_int64 * 3), ("append_indptr", _vp), ("kv_indptr", _vp),
+                ("kv_indices", _vp), ("kv_last_page_len", _vp), ("positions", _vp), ("batch", ctypes.c_int32),
+                ("num_rows", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rope", Rope), ("q", _vp),
+                ("q_out", _vp), ("q_stride", ctypes.c_int64 * 2), ("q_out_stride", ctypes.c_int64 * 2),
+                ("num_q_heads", ctypes.c_int32), ("status", _vp)]
+
+
 def _proto(name, res, args):
     f = getattr(_lib, name)
     f.restype = res
@@ -126,6 +155,11 @@ _splice = _proto("skv_mla_splice", ctypes.c_int, [ctypes.POINTER(SpliceParams), 
 _causal = _proto("skv_causal_tables", ctypes.c_int, [ctypes.c_int32, _i32p, _i32p, _i32p, _i32p, ctypes.c_int32,
                                                      _i32p, _i32p, _i32p, _i32p, _i32p, _i32p, ctypes.c_int64,
                                                      ctypes.POINTER(ctypes.c_int64)])
+_rope_frequencies = _proto("skv_rope_frequencies", ctypes.c_int,
+                           [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
+                            ctypes.c_double, ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_float)])
+_rope_apply = _proto("skv_rope_apply", ctypes.c_int, [ctypes.POINTER(RopeParams), _vp])
+_kv_append = _proto("skv_paged_kv_append", ctypes.c_int, [ctypes.POINTER(AppendParams), _vp])
 _wait_timeout = _proto("skv_test_wait_timeout", ctypes.c_int, [_vp, ctypes.c_int64, _vp])
 _fold = _proto("skv_mla_fold_ratio", ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32])
 _status_str = _proto("skv_status_str", ctypes.c_char_p, [ctypes.c_int32])
@@ -135,7 +169,7 @@ SYMBOLS = ["skv_plan_paged", "skv_paged_attn_fwd", "skv_paged_attn_partial", "sk
            "skv_mla_decode_fwd", "skv_mla_decode_partial", "skv_merge_states", "skv_paged_kv_gather",
            "skv_mla_fold_ratio", "skv_status_str", "skv_version", "skv_paged_attn_fwd_static_scratch",
            "skv_test_wait_timeout", "skv_mla_splice", "skv_causal_tables", "skv_plan_paged_subset",
-           "skv_pod_attn_fwd"]
+           "skv_pod_attn_fwd", "skv_rope_frequencies", "skv_rope_apply", "skv_paged_kv_append"]
 
 
 class SkvError(RuntimeError):
@@ -491,5 +525,6 @@ def library_path() -> str:
     return _LIB_PATH
 
 
+from .serving import paged_kv_append, rope_apply, rope_frequencies  # noqa: E402,F401
 from .runner import (CausalMlaDecode, PagedDecodePipeline, PodAttention, RouteMerge, mla_decode,  # noqa: E402,F401
                      paged_attention, pod_attention, pod_decode_sms)

@@ -1,0 +1,180 @@
+"""Rotary frequencies and the argument checks of skv_rope_apply and skv_paged_kv_append, without a
+GPU: every refusal returns before anything is launched."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import oracle.serving as OS
+import split_kv_merge_b200 as skv
+
+PTR = 0x10000  # never dereferenced: a refused call launches nothing
+
+
+def _rope_params(**kw):
+    rope = dict(dim=64, layout=0, theta=10000.0, inv_freq_h=None, mscale=1.0)
+    rope.update({k[5:]: v for k, v in kw.items() if k.startswith("rope_")})
+    p = dict(q=PTR, q_out=2 * PTR, k=3 * PTR, k_out=4 * PTR, q_stride=(512, 64), q_out_stride=(512, 64),
+             k_stride=(128, 64), k_out_stride=(128, 64), positions=5 * PTR, num_tokens=3, num_q_heads=8, num_k_heads=2,
+             head_dim=64, dtype=skv.BF16, inverse=0)
+    p.update({k: v for k, v in kw.items() if not k.startswith("rope_")})
+    return skv.RopeParams(rope=skv.Rope(**rope), **p)
+
+
+def _append_params(**kw):
+    rope = dict(dim=64, layout=1, theta=10000.0, inv_freq_h=None, mscale=1.0)
+    rope.update({k[5:]: v for k, v in kw.items() if k.startswith("rope_")})
+    p = dict(k=PTR, v=PTR, k_row_stride=(128, 64), v_row_stride=(128, 64), k_cache=PTR, v_cache=PTR,
+             k_stride=(2048, 128, 64), v_stride=(2048, 128, 64), kv_dtype=skv.BF16, kv_scale=1.0, block_tokens=0,
+             k_scale=PTR, v_scale=PTR, k_scale_stride=(2, 2, 1), v_scale_stride=(2, 2, 1), append_indptr=PTR,
+             kv_indptr=PTR, kv_indices=PTR, kv_last_page_len=PTR, positions=None, batch=2, num_rows=5, num_pages=9,
+             page_size=16, num_kv_heads=2, head_dim=64, q=PTR, q_out=2 * PTR, q_stride=(512, 64),
+             q_out_stride=(512, 64), num_q_heads=8, status=None)
+    p.update({k: v for k, v in kw.items() if not k.startswith("rope_")})
+    return skv.AppendParams(rope=skv.Rope(**rope), **p)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(num_tokens=-1), skv.ERR_INVALID), (dict(num_q_heads=-1), skv.ERR_INVALID), (dict(head_dim=0), skv.ERR_INVALID),
+    (dict(head_dim=68), skv.ERR_UNSUPPORTED), (dict(head_dim=2048), skv.ERR_UNSUPPORTED),
+    (dict(dtype=skv.E4M3), skv.ERR_UNSUPPORTED), (dict(rope_dim=-16), skv.ERR_INVALID),
+    (dict(rope_dim=80), skv.ERR_INVALID), (dict(rope_dim=24), skv.ERR_UNSUPPORTED),
+    (dict(head_dim=512, rope_dim=512), skv.ERR_UNSUPPORTED), (dict(rope_layout=2), skv.ERR_INVALID),
+    (dict(rope_theta=0.0), skv.ERR_INVALID), (dict(rope_theta=math.inf), skv.ERR_INVALID),
+    (dict(rope_mscale=0.0), skv.ERR_INVALID), (dict(rope_mscale=math.nan), skv.ERR_INVALID),
+    (dict(q=None), skv.ERR_INVALID), (dict(k_out=None), skv.ERR_INVALID), (dict(positions=None), skv.ERR_INVALID),
+    (dict(q=PTR + 2), skv.ERR_ALIGNMENT), (dict(q_stride=(516, 64)), skv.ERR_ALIGNMENT),
+    (dict(k_stride=(-128, 64)), skv.ERR_INVALID), (dict(q_out=PTR, q_out_stride=(1024, 64)), skv.ERR_INVALID),
+    (dict(num_tokens=0), skv.OK), (dict(num_q_heads=0, num_k_heads=0), skv.OK),
+])
+def test_rope_apply_refusals(change, code):
+    assert skv._rope_apply(ctypes.byref(_rope_params(**change)), None) == code
+
+
+def test_rope_apply_refuses_frequencies_that_are_not_finite():
+    f = np.ones(32)
+    f[7] = np.nan
+    assert skv._rope_apply(ctypes.byref(_rope_params(rope_inv_freq_h=f.ctypes.data)), None) == skv.ERR_INVALID
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(batch=-1), skv.ERR_INVALID), (dict(page_size=0), skv.ERR_INVALID), (dict(num_kv_heads=0), skv.ERR_INVALID),
+    (dict(head_dim=96), skv.ERR_UNSUPPORTED), (dict(kv_dtype=skv.F32), skv.ERR_UNSUPPORTED),
+    (dict(kv_dtype=skv.I8), skv.ERR_UNSUPPORTED), (dict(kv_dtype=skv.E4M3, kv_scale=0.0), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.E4M3, kv_scale=math.nan), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.E4M3, kv_scale=1e-40), skv.ERR_INVALID), (dict(block_tokens=16), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.I8, block_tokens=5), skv.ERR_INVALID), (dict(kv_dtype=skv.I8, block_tokens=-1), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.I8, block_tokens=512, page_size=512), skv.ERR_UNSUPPORTED),
+    (dict(kv_dtype=skv.I8, block_tokens=16, k_scale=None), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.I8, block_tokens=16, v_scale_stride=(2, -2, 1)), skv.ERR_INVALID),
+    (dict(kv_dtype=skv.I8, block_tokens=16, k_stride=(2048, 128, 72)), skv.ERR_ALIGNMENT),
+    (dict(rope_dim=40), skv.ERR_UNSUPPORTED), (dict(rope_layout=-1), skv.ERR_INVALID), (dict(k=None), skv.ERR_INVALID),
+    (dict(v_row_stride=(128, 60)), skv.ERR_ALIGNMENT), (dict(append_indptr=None), skv.ERR_INVALID),
+    (dict(kv_indices=None), skv.ERR_INVALID), (dict(k_cache=PTR + 8), skv.ERR_ALIGNMENT),
+    (dict(v_stride=(-2048, 128, 64)), skv.ERR_INVALID), (dict(q=None), skv.ERR_INVALID),
+    (dict(q_out=PTR, q_out_stride=(520, 64)), skv.ERR_INVALID), (dict(num_rows=0), skv.OK), (dict(batch=0), skv.OK),
+])
+def test_append_refusals(change, code):
+    assert skv._kv_append(ctypes.byref(_append_params(**change)), None) == code
+
+
+def test_null_params():
+    assert skv._rope_apply(None, None) == skv.ERR_INVALID
+    assert skv._kv_append(None, None) == skv.ERR_INVALID
+
+
+def test_python_checks():
+    torch = pytest.importorskip("torch")
+    x, pos = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for bad in (lambda: skv.rope_apply(x, None, pos),                         # not on a CUDA device
+                lambda: skv.rope_apply(None, None, pos), lambda: skv.rope_apply(x.half(), None, pos),
+                lambda: skv.rope_apply(x, None, pos.long()), lambda: skv.rope_apply(x, None, pos[:2]),
+                lambda: skv.rope_frequencies(64, scaling="cubic")):
+        with pytest.raises(ValueError):
+            bad()
+    cache, ip = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for kw in (dict(k_scale=torch.zeros(4, 1, 2)), dict(q=torch.zeros(3, 4, 32)), dict(num_pages=5),
+               dict(positions=pos[:1]), dict()):
+        with pytest.raises(ValueError):
+            skv.paged_kv_append(x, x, cache, cache, ip, ip, ip, ip[:1], **kw)
+
+
+def _wavelength_turns(f, context):
+    return context * f / (2 * math.pi)
+
+
+def test_rope_frequencies():
+    dim, theta, ctx, factor = 128, 10000.0, 4096, 8.0
+    plain = np.array([theta ** (-2 * i / dim) for i in range(dim // 2)])
+    f, m = skv.rope_frequencies(dim, theta)
+    assert m == 1.0 and np.allclose(f, plain, rtol=1e-14, atol=0)
+    f, _ = skv.rope_frequencies(dim, theta, "linear", factor)
+    assert np.allclose(f, plain / factor, rtol=1e-14, atol=0)
+    # a larger base that leaves the fastest pair and divides the slowest by the factor
+    f, _ = skv.rope_frequencies(dim, theta, "ntk", factor)
+    assert f[0] == 1.0 and np.isclose(f[-1], plain[-1] / factor, rtol=1e-12)
+    for name, low, high in (("yarn", 1.0, 32.0), ("bands", 1.0, 4.0)):
+        f, m = skv.rope_frequencies(dim, theta, name, factor, ctx)
+        assert np.isclose(m, 0.1 * math.log(factor) + 1 if name == "yarn" else 1.0, rtol=1e-6)
+        turns = _wavelength_turns(plain, ctx)
+        kept, stretched = turns > high * 1.2, turns < low / 1.2   # a pair of the ramp's rounding either side
+        assert kept.any() and stretched.any()
+        assert np.allclose(f[kept], plain[kept], rtol=1e-14) and np.allclose(f[stretched], plain[stretched] / factor)
+        assert np.all(np.diff(f) < 0) and np.all(f <= plain) and np.all(f >= plain / factor * (1 - 1e-12))
+    i = int(np.argmin(np.abs(_wavelength_turns(plain, ctx) - 2.0)))
+    kept = (_wavelength_turns(plain, ctx)[i] - 1) / 3
+    assert np.isclose(skv.rope_frequencies(dim, theta, "bands", factor, ctx)[0][i],
+                      plain[i] * (kept + (1 - kept) / factor), rtol=1e-12)
+
+
+@pytest.mark.parametrize("args", [(63,), (0,), (64, 1.0), (64, 1e4, 9), (64, 1e4, 1, 0.5), (2, 1e4, 2, 2.0),
+                                  (64, 1e4, 3, 2.0, 0.0), (64, 1e4, 3, 2.0, 4096, 4.0, 4.0), (64, math.nan)])
+def test_rope_frequencies_refusals(args):
+    full = list(args) + [1e4, 0, 1.0, 4096.0, 1.0, 32.0][len(args) - 1:]
+    assert skv._rope_frequencies(*full, None, None) == skv.ERR_INVALID
+
+
+def test_oracle_rotation_is_a_rotation():
+    """The oracle's rotation against complex multiplication, and its reduction of far angles."""
+    rng = np.random.default_rng(3)
+    x, pos, f = rng.standard_normal((5, 2, 24)), [0, 1, -7, 12345, 2 ** 30 + 1], np.array([1.0, 0.37, 1e-3, 2.5, 0.01, 7e-5, 0.2, 3.0])
+    for layout in ("interleaved", "halves"):
+        a, b = OS.pair_columns(layout, 16)
+        y = OS.rotate(x, pos, f, layout, 1.5)
+        z = (x[..., a] + 1j * x[..., b]) * 1.5 * np.exp(1j * np.remainder(np.outer(pos, f).astype(np.longdouble), 2 * np.pi).astype(float))[:, None]
+        assert np.allclose(y[:4, :, a], z.real[:4], atol=1e-10) and np.allclose(y[:4, :, b], z.imag[:4], atol=1e-10)
+        assert np.array_equal(y[..., 16:], x[..., 16:])
+        assert np.allclose(OS.rotate(y, pos, f, layout, 1 / 1.5, inverse=True), x, atol=1e-12)
+
+
+def c_layout(pairs):
+    """Sizes and field offsets of C structs of include/splitkv.h, compiled with gcc, against ctypes."""
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "splitkv.h"', "int main(void) {"]
+    for cls, name in pairs:
+        lines.append(f'  printf("%zu\\n", sizeof({name}));')
+        lines += [f'  printf("%zu %zu\\n", offsetof({name}, {f}), sizeof((({name}*)0)->{f}));' for f, _ in cls._fields_]
+    d = os.path.join(root, "_build", "c_tests")
+    os.makedirs(d, exist_ok=True)
+    src, exe = os.path.join(d, "serving_layout.c"), os.path.join(d, "serving_layout")
+    with open(src, "w") as f:
+        f.write("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), src, "-o", exe], check=True)
+    got = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
+    want = []
+    for cls, _ in pairs:
+        want.append(str(ctypes.sizeof(cls)))
+        want += [f"{getattr(cls, f).offset} {getattr(cls, f).size}" for f, _ in cls._fields_]
+    return got, want
+
+
+def test_struct_layouts():
+    import shutil
+    if shutil.which("gcc") is None:
+        pytest.skip("needs a C compiler")
+    got, want = c_layout([(skv.Rope, "skv_rope"), (skv.RopeParams, "skv_rope_params"),
+                          (skv.AppendParams, "skv_append_params")])
+    assert got == want

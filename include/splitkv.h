@@ -24,6 +24,9 @@
  *                       batch_pod.cu: prefill and decode work fused in one kernel).
  *   skv_causal_tables   Host planner that turns causal / multi-token attention into a prefix
  *                       call, a diagonal call over token rows and an exact merge.
+ *   skv_paged_attn_scaled_fwd  GQA attention over a paged cache held in 8 bits (e4m3 or int8) with
+ *                       one scale for each block of tokens and KV head, optionally causal among
+ *                       a request's query tokens.
  *   skv_rope_apply      Rotary positions of queries and keys (both pair layouts, part of the head,
  *                       frequencies stretched for long contexts by skv_rope_frequencies).
  *   skv_paged_kv_append New keys and values into the paged cache, rotated on the way; the cache
@@ -108,8 +111,9 @@ typedef struct {
   int32_t kernel;           /* kernel variant the dispatcher picked (informational): 1 GQA on  */
                             /*   CUDA cores, 2 GQA tensor-core decode per KV head, 3 GQA      */
                             /*   tensor-core decode over all KV heads, 4 GQA tensor-core      */
-                            /*   prefill (128 query rows), 11 MLA on CUDA cores, 12 / 13 / 14 */
-                            /*   MLA tensor cores with 16 / 32 / 64 query rows per tile       */
+                            /*   prefill (128 query rows), 5 GQA decode over a block-scaled   */
+                            /*   8-bit cache, 11 MLA on CUDA cores, 12 / 13 / 14 MLA tensor    */
+                            /*   cores with 16 / 32 / 64 query rows per tile                  */
   int32_t q_tile;           /* query tokens per work item (MLA: the fold ratio F)             */
   int32_t plan_words;       /* int32 words of the plan actually used                          */
   int32_t max_splits;       /* largest split count of any request                             */
@@ -417,6 +421,41 @@ typedef struct {
 
 SKV_API skv_status skv_mla_splice(const skv_splice_params* p, const skv_splice_chunk* chunks_h,
                                   int32_t num_chunks, skv_stream_t stream);
+
+/* -------------------------------------------------------------------------------------------
+ * skv_plan_paged_scaled / skv_paged_attn_scaled_fwd -- GQA attention over a paged cache of 8-bit
+ *   codes with block scales, as skv_paged_kv_append writes it:
+ *     k(page, slot, head, :) = k_scale(page, slot / block_tokens, head) * code, v likewise.
+ *   Any page size, any KV head count and any group Hq / Hk; head_dim 64 or 128.  With `causal` the
+ *   n query tokens of a request are its last n positions and query token i sees keys
+ *   t <= L - n + i; a token that sees none gets O = 0, LSE = -inf.  Made for a few query tokens
+ *   per request (decode, drafted tokens); every tile of 8 or 16 query rows (tokens x group)
+ *   streams the request's keys again.
+ *   Slots past a request's length may hold anything, NaN codes and scales included.  A key that
+ *   some query token of its request sees must have finite K, V and scales: where it is masked
+ *   for another token of the request its weight is 0, and 0 x NaN is not 0.
+ *   Planning as skv_plan_paged (same policies); the plan belongs to one `causal` setting and
+ *   to these lengths.  Run it with skv_paged_attn_scaled_fwd only.
+ * ----------------------------------------------------------------------------------------- */
+SKV_API skv_status skv_plan_paged_scaled(int32_t batch, const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
+                                         const int32_t* kv_last_page_len_h, int32_t page_size,
+                                         int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t causal, int32_t policy, int32_t param,
+                                         const int32_t* split_indptr_h, const int32_t* split_bounds_h,
+                                         int32_t* plan_h, int64_t plan_capacity, skv_plan_info* info);
+
+typedef struct {
+  skv_paged_params base;    /* kv_dtype SKV_E4M3 or SKV_I8 (strides in elements, multiples of 16);   */
+                            /*   kv_scale is not read                                              */
+  const float* k_scale;     /* k_scale(page, block, head) = k_scale[page*s[0] + block*s[1] +           */
+  const float* v_scale;     /*   head*s[2]], any strides                                            */
+  int64_t k_scale_stride[3];
+  int64_t v_scale_stride[3];
+  int32_t block_tokens;     /* tokens that share a scale: a divisor of page_size                      */
+} skv_paged_scaled_params;
+
+SKV_API skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* p, const int32_t* plan_d,
+                                             const skv_plan_info* info, skv_stream_t stream);
 
 /* -------------------------------------------------------------------------------------------
  * Rotary positions.  Pair p of a head's first `dim` values turns by the angle

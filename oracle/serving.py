@@ -76,3 +76,41 @@ def append_blocks(x, values, scales, rows, block: int, qmax: float):
         for t, slot in members:
             values[page, slot] = x[t]
     return values, scales
+
+
+def attend(q, k, v, limits, sm_scale: float):
+    """One KV head's rows q [R, D] over keys k [L, D], values v [L, D]; row i sees the first limits[i] keys.
+    Returns O, LSE, sum_t p_t |v_t| (what rounding the weights acts on) and max_t sm_scale |q| . |k_t|."""
+    if not len(k):
+        z = np.zeros_like(q)
+        return z, np.full(len(q), -np.inf), z.copy(), np.zeros(len(q))
+    s = sm_scale * (q @ k.T)
+    s[np.arange(len(k))[None, :] >= np.asarray(limits)[:, None]] = -np.inf
+    m = s.max(axis=1)
+    base = np.where(np.isneginf(m), 0.0, m)
+    p = np.exp(s - base[:, None])
+    l = p.sum(axis=1)
+    p /= np.where(l > 0, l, 1.0)[:, None]
+    with np.errstate(divide="ignore"):
+        lse = np.where(l > 0, base + np.log(l), -np.inf)
+    return p @ v, lse, p @ np.abs(v), sm_scale * (np.abs(q) @ np.abs(k).T).max(axis=1)
+
+
+def packed_attention(q, k_of, v_of, qo_indptr, lengths, hk: int, causal: bool, sm_scale: float, requests=None):
+    """Attention of packed queries q [T, Hq, D]; k_of(r) / v_of(r) give request r's keys [L_r, Hk, D].  With
+    ``causal`` the n query tokens of a request are its last n positions.  Returns O, LSE, weight scale
+    and score scale of ``attend`` for every row (NaN where a request is not asked for)."""
+    T, hq, d = q.shape
+    g = hq // hk
+    o, a = np.full((T, hq, d), np.nan), np.full((T, hq, d), np.nan)
+    lse, mag = np.full((T, hq), np.nan), np.full((T, hq), np.nan)
+    for r in range(len(lengths)) if requests is None else requests:
+        q0, q1, L = int(qo_indptr[r]), int(qo_indptr[r + 1]), int(lengths[r])
+        if q1 == q0:
+            continue
+        k, v, n = k_of(r), v_of(r), q1 - q0
+        limits = L - n + 1 + np.arange(n) if causal else np.full(n, L)
+        for h in range(hq):
+            o[q0:q1, h], lse[q0:q1, h], a[q0:q1, h], mag[q0:q1, h] = attend(q[q0:q1, h], k[:, h // g], v[:, h // g],
+                                                                            limits, sm_scale)
+    return o, lse, a, mag

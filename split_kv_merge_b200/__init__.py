@@ -8,6 +8,7 @@ there is no fallback path.
 Functions mirror the C ABI in include/splitkv.h:
 ``plan_paged``, ``paged_attn_fwd``, ``pod_attn_fwd``, ``plan_mla``, ``mla_decode_fwd``, ``merge_states``,
 ``paged_kv_gather``, ``mla_splice``, ``rope_frequencies``, ``rope_apply``, ``paged_kv_append``,
+``plan_paged_scaled``, ``paged_attention_scaled``,
 ``mla_fold_ratio``, ``status_str``, ``version``.
 """
 from __future__ import annotations
@@ -87,6 +88,11 @@ class SpliceChunk(ctypes.Structure):
                 ("delta_pos", ctypes.c_int64)]
 
 
+class PagedScaledParams(ctypes.Structure):
+    _fields_ = [("base", PagedParams), ("k_scale", _vp), ("v_scale", _vp), ("k_scale_stride", ctypes.c_int64 * 3),
+                ("v_scale_stride", ctypes.c_int64 * 3), ("block_tokens", ctypes.c_int32)]
+
+
 class Rope(ctypes.Structure):
     _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("theta", ctypes.c_double),
                 ("inv_freq_h", _vp), ("mscale", ctypes.c_float)]
@@ -155,6 +161,10 @@ _splice = _proto("skv_mla_splice", ctypes.c_int, [ctypes.POINTER(SpliceParams), 
 _causal = _proto("skv_causal_tables", ctypes.c_int, [ctypes.c_int32, _i32p, _i32p, _i32p, _i32p, ctypes.c_int32,
                                                      _i32p, _i32p, _i32p, _i32p, _i32p, _i32p, ctypes.c_int64,
                                                      ctypes.POINTER(ctypes.c_int64)])
+_plan_scaled = _proto("skv_plan_paged_scaled", ctypes.c_int, [ctypes.c_int32, _i32p, _i32p, _i32p] +
+                      [ctypes.c_int32] * 7 + [_i32p, _i32p, _i32p, ctypes.c_int64, ctypes.POINTER(PlanInfo)])
+_scaled_fwd = _proto("skv_paged_attn_scaled_fwd", ctypes.c_int, [ctypes.POINTER(PagedScaledParams), _vp,
+                                                                 ctypes.POINTER(PlanInfo), _vp])
 _rope_frequencies = _proto("skv_rope_frequencies", ctypes.c_int,
                            [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                             ctypes.c_double, ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_float)])
@@ -169,7 +179,8 @@ SYMBOLS = ["skv_plan_paged", "skv_paged_attn_fwd", "skv_paged_attn_partial", "sk
            "skv_mla_decode_fwd", "skv_mla_decode_partial", "skv_merge_states", "skv_paged_kv_gather",
            "skv_mla_fold_ratio", "skv_status_str", "skv_version", "skv_paged_attn_fwd_static_scratch",
            "skv_test_wait_timeout", "skv_mla_splice", "skv_causal_tables", "skv_plan_paged_subset",
-           "skv_pod_attn_fwd", "skv_rope_frequencies", "skv_rope_apply", "skv_paged_kv_append"]
+           "skv_pod_attn_fwd", "skv_rope_frequencies", "skv_rope_apply", "skv_paged_kv_append",
+           "skv_plan_paged_scaled", "skv_paged_attn_scaled_fwd"]
 
 
 class SkvError(RuntimeError):
@@ -316,6 +327,17 @@ def plan_mla(batch_q_len: int, kv_indptr, kv_last_page_len, page_size: int, num_
     return _plan(_plan_mla, lambda pol: (b, batch_q_len, _ptr_i32(ki), _ptr_i32(la), page_size, num_heads, kd,
                                          pol, param),
                  policy, split_page_start, "skv_plan_mla")
+
+
+def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, num_qo_heads: int, num_kv_heads: int,
+                      head_dim: int, causal: bool = False, policy="balanced", param: int = 0,
+                      split_page_start: Optional[Sequence[Sequence[int]]] = None) -> Plan:
+    """Host planner (skv_plan_paged_scaled) for attention over an 8-bit cache with block scales."""
+    qo, ki, la = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_last_page_len)
+    b = len(ki) - 1
+    return _plan(_plan_scaled, lambda pol: (b, _ptr_i32(qo), _ptr_i32(ki), _ptr_i32(la), page_size, num_qo_heads,
+                                            num_kv_heads, head_dim, int(causal), pol, param),
+                 policy, split_page_start, "skv_plan_paged_scaled")
 
 
 # ----------------------------------------------------------------------------- launches
@@ -525,6 +547,6 @@ def library_path() -> str:
     return _LIB_PATH
 
 
-from .serving import paged_kv_append, rope_apply, rope_frequencies  # noqa: E402,F401
+from .serving import (paged_attention_scaled, paged_kv_append, rope_apply, rope_frequencies)  # noqa: E402,F401
 from .runner import (CausalMlaDecode, PagedDecodePipeline, PodAttention, RouteMerge, mla_decode,  # noqa: E402,F401
                      paged_attention, pod_attention, pod_decode_sms)

@@ -563,6 +563,90 @@ skv_status skv_paged_attn_fwd(const skv_paged_params* p, const int32_t* plan_d,
                         p->lse, stream);
 }
 
+skv_status skv_plan_paged_scaled(int32_t batch, const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
+                                 const int32_t* kv_last_page_len_h, int32_t page_size, int32_t num_qo_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, int32_t causal, int32_t policy, int32_t param,
+                                 const int32_t* split_indptr_h, const int32_t* split_bounds_h, int32_t* plan_h,
+                                 int64_t plan_capacity, skv_plan_info* info) try {
+  if (info != nullptr) std::memset(info, 0, sizeof(*info));
+  if (qo_indptr_h == nullptr || num_qo_heads < 1 || num_kv_heads < 1) return SKV_ERR_INVALID;
+  if (num_qo_heads % num_kv_heads != 0) return SKV_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return SKV_ERR_UNSUPPORTED;
+  if (num_qo_heads > 65535) return SKV_ERR_UNSUPPORTED;
+  std::vector<ReqShape> req;
+  skv_status st = check_table_h(batch, kv_indptr_h, kv_last_page_len_h, page_size, req);
+  if (st != SKV_OK) return st;
+  if (batch > 0 && qo_indptr_h[0] != 0) return SKV_ERR_INVALID;
+  std::vector<int64_t> kv_len(batch);
+  int32_t max_q = 1;
+  for (int32_t r = 0; r < batch; ++r) {
+    req[r].q_start = qo_indptr_h[r];
+    req[r].q_len = qo_indptr_h[r + 1] - qo_indptr_h[r];
+    if (req[r].q_len < 0) return SKV_ERR_INVALID;
+    max_q = std::max(max_q, req[r].q_len);
+    kv_len[r] = req[r].n_pages == 0 ? 0 : (int64_t)(req[r].n_pages - 1) * page_size + kv_last_page_len_h[r];
+  }
+  const int32_t group = num_qo_heads / num_kv_heads, units = gqa_scaled_units(num_kv_heads, group);
+  PersistOpts po;
+  po.page_size = page_size;
+  po.tile_tokens = gqa_scaled_tile_tokens(num_kv_heads);
+  po.flat_ctas = std::max(1, device_sms(policy == SKV_SPLIT_BALANCED ? param : 0) / units);
+  po.piece_cost = 2;
+  st = plan_common(batch, req, kv_len, gqa_scaled_q_tile(group, max_q), 1, 8, policy, param, split_indptr_h,
+                   split_bounds_h, KERNEL_GQA_SCALED, po, plan_h, plan_capacity, info);
+  if (st != SKV_OK) return st;
+  // the keys an item's first query token sees (the kernel adds the token's place in the item)
+  WorkItem* work = reinterpret_cast<WorkItem*>(plan_h);
+  for (int32_t i = 0; i < info->num_work; ++i) {
+    const int32_t r = work[i].r;
+    const int64_t seen = kv_len[r] - req[r].q_len + (work[i].q_start - req[r].q_start) + 1;
+    work[i].split = causal ? (int32_t)std::max<int64_t>(seen, -(1 << 30)) : 1 << 30;
+    if (!causal && kv_len[r] > (1 << 30)) return SKV_ERR_UNSUPPORTED;
+  }
+  return SKV_OK;
+} catch (...) {
+  return SKV_ERR_INVALID;  // out of host memory
+}
+
+skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* sp, const int32_t* plan_d,
+                                     const skv_plan_info* info, skv_stream_t stream) {
+  if (sp == nullptr) return SKV_ERR_INVALID;
+  const skv_paged_params* p = &sp->base;
+  skv_status st = check_plan(plan_d, info);
+  if (st != SKV_OK) return st;
+  if (info->kernel != KERNEL_GQA_SCALED) return SKV_ERR_INVALID;
+  if (p->batch < 0 || p->total_q < 0 || p->page_size < 1 || p->num_pages < 0) return SKV_ERR_INVALID;
+  if (p->num_qo_heads < 1 || p->num_kv_heads < 1 || p->num_qo_heads % p->num_kv_heads) return SKV_ERR_INVALID;
+  if (p->head_dim != 64 && p->head_dim != 128) return SKV_ERR_UNSUPPORTED;
+  if (p->num_qo_heads > 65535) return SKV_ERR_UNSUPPORTED;
+  if (p->kv_dtype != SKV_E4M3 && p->kv_dtype != SKV_I8) return SKV_ERR_UNSUPPORTED;
+  if (p->o_dtype != SKV_F32 && p->o_dtype != SKV_BF16) return SKV_ERR_UNSUPPORTED;
+  if (sp->block_tokens < 1 || p->page_size % sp->block_tokens != 0) return SKV_ERR_INVALID;
+  if (info->num_work == 0) return SKV_OK;  // no query rows: nothing to launch
+  if (!p->q || !p->k_cache || !p->v_cache || !p->kv_indptr || !p->kv_indices || !p->kv_last_page_len || !p->o ||
+      !sp->k_scale || !sp->v_scale)
+    return SKV_ERR_INVALID;
+  for (int i = 0; i < 3; ++i) {
+    if (p->k_stride[i] < 0 || p->v_stride[i] < 0 || sp->k_scale_stride[i] < 0 || sp->v_scale_stride[i] < 0)
+      return SKV_ERR_INVALID;
+    if ((p->k_stride[i] % 16) || (p->v_stride[i] % 16)) return SKV_ERR_ALIGNMENT;
+  }
+  if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->o))
+    return SKV_ERR_ALIGNMENT;
+  if (info->num_partial_rows > 0 && (!p->o_part || !p->lse_part)) return SKV_ERR_WORKSPACE;
+  if (!aligned16(p->o_part)) return SKV_ERR_ALIGNMENT;
+  // a tile holds 16 query rows, or one token of a larger group
+  const int64_t group = p->num_qo_heads / p->num_kv_heads;
+  if (info->q_tile > 1 && info->q_tile * group > 16) return SKV_ERR_INVALID;
+  if (info->num_ctas < 1 || info->cta_offset < 8LL * info->num_work + 4LL * info->num_merge_rows)
+    return SKV_ERR_INVALID;
+  st = cuda_status(launch_gqa_scaled(*sp, reinterpret_cast<const WorkItem*>(plan_d), plan_d + info->cta_offset,
+                                     info->num_ctas, info->q_tile, reinterpret_cast<cudaStream_t>(stream)));
+  if (st != SKV_OK) return st;
+  return skv_merge_plan(p->o_part, p->lse_part, plan_d, info, p->num_qo_heads, p->head_dim, p->o, p->o_dtype, p->lse,
+                        stream);
+}
+
 skv_status skv_pod_attn_fwd(const skv_paged_params* p, const int32_t* decode_plan_d,
                             const skv_plan_info* decode_info, const int32_t* prefill_plan_d,
                             const skv_plan_info* prefill_info, float* prefill_o_part, float* prefill_lse_part,

@@ -1,0 +1,662 @@
+// GQA attention over a paged cache held in 8 bits (e4m3 or int8 codes) with one fp32 scale for each
+// block of tokens and KV head:  k = ks * code, v = vs * code,
+//   s_t = sm_scale (q . kcode_t) ks_t,   O = sum_t softmax(s)_t vs_t vcode_t,   LSE = ln sum_t e^{s_t}.
+// The scales leave both products: ks multiplies the finished scores, vs the softmax weights, so the
+// matrix instructions run on the codes themselves, which f16 holds exactly (e4m3: 4 significant
+// bits, 2^-9 .. 448; int8: integers).
+//
+// Bound by HBM: 2 Hk D bytes per token.  One CTA takes `hc` KV heads (the largest of 8, 4, 2, 1 that
+// divides Hk) of a slice of the batch's tokens (persistent, slices cut equal by the planner), so a
+// token's rows of those heads are read together.  Four producer warps fill a ring of shared-memory
+// stages with cp.async (any page size, any 16-byte strides; rows past the end are zero-filled
+// without reading); eight consumer warps each own one head and 32 tokens of a stage and keep their
+// own running maximum, sum and O, merged across the warps of a head when a work item ends.
+//
+// Decode has few query rows per KV head (R = group x query tokens <= 16), far below the 128 rows of
+// the tcgen05 shapes, and each code needs widening in registers anyway, so the products are
+// m16n8k16 f16 MMAs whose operands come straight from registers: S[rows, tokens] = Q . K^T leaves
+// its accumulators exactly where the A operand of O[rows, dims] += P . V wants them.
+//   - K: lane (g, t) reads 16-byte chunks t and t + 4 of its token's row; the dims of a k-step are
+//     permuted to what one lane holds, Q is loaded under the same permutation.
+//   - V: a B operand pairs two tokens of one dim.  Lane (g, t) reads the same 16 dims of four tokens
+//     and interleaves bytes of two tokens (one byte permute per two pairs) before widening; output
+//     dims are permuted, and come out as runs of 16 for one lane.
+//   - chunks are XOR-swizzled by token so that the eight lanes of a 128-byte wavefront hit
+//     different banks, for K and V alike.
+// Precision: Q (bf16) moves to f16 after a power-of-two scale per row (largest element to
+// [2^14, 2^15): exact for every element of at least 2^-31 of the row's largest).  Weights are formed as
+// p * (vs / vref), vref the largest vs of the 32 tokens, in f16 (11 bits; the maximum is raised
+// once a score passes it by 2^8, so p <= 2^8), and the partial product is scaled by vref in fp32.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "tc_ptx.cuh"
+
+namespace skv {
+
+namespace {
+
+constexpr int kConsumers = 8;                 // warps
+constexpr int kProducers = 4;                 // warps
+constexpr int kThreads = 32 * (kConsumers + kProducers);
+constexpr int kWarpTokens = 32;               // tokens of a stage that one consumer warp takes
+constexpr float kRaise = 8.f;
+
+template <int D>
+struct Smem {
+  static constexpr int rows = kConsumers * kWarpTokens;           // (head, token) rows of a stage
+  static constexpr int kv = rows * D;                             // bytes of K (and of V)
+  static constexpr int scales = rows * 4;                         // of K (and of V)
+  static constexpr int stage = 2 * (kv + scales);
+  static constexpr int stages = D == 128 ? 3 : 5;
+  static constexpr int merge = stages * stage;                    // [4 warps][8 rows][D] floats
+  static constexpr int stat = merge + 4 * 8 * D * 4;              // [4 warps][16 rows] float2 (m, l)
+  static constexpr int bars = stat + 4 * 16 * 8;
+  static constexpr int misc = bars + 2 * stages * 8;
+  static constexpr int total = misc + 16;
+};
+static_assert(Smem<128>::total <= 232448 && Smem<64>::total <= 232448, "227 KB opt-in shared memory");
+
+struct SArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* ks;
+  const float* vs;
+  int64_t k0, k1, k2, v0, v1, v2;
+  int64_t ks0, ks1, ks2, vs0, vs1, vs2;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last;
+  const WorkItem* work;
+  const int32_t* cta_indptr;
+  int num_pages, page_size, block_tokens, hq, hk, g;
+  int hc_log2;        // KV heads of a CTA
+  int head_groups;    // hk / hc
+  int row_groups;     // ceil(g / 16) when one token's rows exceed a tile, else 1
+  float scale_log2;
+  void* o;
+  float* lse;
+  float* o_part;
+  float* lse_part;
+  int32_t* status;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// this thread's earlier cp.asyncs arrive on the barrier when they have landed
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// four codes -> two f16 pairs, exact
+template <bool I8>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (I8) {
+    // bytes u = code + 128 under the exponent of 1024: the f16 1024 + u; minus 1152 is the code
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// Token of an 8-token group that column c of a score tile holds, and the swizzle of a token's row:
+// chosen so that the lanes of one shared-memory wavefront hit different banks (see the top).
+template <int D>
+__device__ __forceinline__ constexpr int col_token(int c) {
+  return D == 128 ? ((c & 1) << 2) | (c >> 1) : c;
+}
+template <int D>
+__device__ __forceinline__ constexpr int swizzle(int tok) {
+  return D == 128 ? tok & 7 : (tok >> 1) & 3;
+}
+
+struct Range {
+  int t0, t1, tiles;
+};
+__device__ __forceinline__ Range item_range(const SArgs& a, const WorkItem& w, int tile_tokens) {
+  Range r;
+  const int len = request_len(a.kv_indptr, a.last, w.r, a.page_size);
+  r.t0 = w.page_begin * a.page_size;
+  // w.split holds the first query token's key limit (causal), or a limit beyond any length
+  r.t1 = min(min(w.page_end * a.page_size, len), w.split + w.q_count - 1);
+  r.tiles = r.t1 > r.t0 ? (r.t1 - r.t0 + tile_tokens - 1) / tile_tokens : 0;
+  return r;
+}
+
+template <bool I8, int D, bool WIDE, typename OutT>
+__global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_constant__ SArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using S = Smem<D>;
+  constexpr int kChunks = D / 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  tc::grid_launch_dependents();  // the merge pass may be scheduled; it waits for this grid
+  const uint32_t sbase = tc::smem_u32(smem);
+  const uint32_t bar0 = sbase + S::bars;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S::stages + s); };
+  if (tid == 0) {
+    for (int s = 0; s < S::stages; ++s) {
+      tc::mbar_init(full_bar(s), 32 * kProducers);
+      tc::mbar_init(empty_bar(s), kConsumers);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+
+  const int unit = blockIdx.x % (a.head_groups * a.row_groups), cta = blockIdx.x / (a.head_groups * a.row_groups);
+  const int hc = 1 << a.hc_log2, h0 = (unit % a.head_groups) * hc, row0 = (unit / a.head_groups) * 16;
+  const int tile_tokens = (kConsumers * kWarpTokens) >> a.hc_log2;
+  const int w_begin = a.cta_indptr[cta], w_end = a.cta_indptr[cta + 1];
+
+  if (warp >= kConsumers) {
+    // ================================================================================ producers
+    const int pw = warp - kConsumers;
+    const int mine = tile_tokens / kProducers;  // 8, 16, 32 or 64 tokens of a tile for this warp
+    int it = 0;
+    bool ok = true;
+    for (int wi = w_begin; wi < w_end && ok; ++wi) {
+      const WorkItem w = a.work[wi];
+      const Range rg = item_range(a, w, tile_tokens);
+      const int32_t* ids = a.kv_indices + a.kv_indptr[w.r];
+      // page ids of this warp's tokens, one tile ahead of their use
+      int next[2];
+      auto fetch_ids = [&](int tile) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int tok = rg.t0 + tile * tile_tokens + pw * mine + b * 32 + lane;
+          next[b] = (b * 32 + lane < mine && tok < rg.t1) ? __ldg(ids + tok / a.page_size) : 0;
+        }
+      };
+      if (rg.tiles > 0) fetch_ids(0);
+      for (int tile = 0; tile < rg.tiles; ++tile, ++it) {
+        const int st = it % S::stages;
+        int id[2] = {next[0], next[1]};
+        if (tile + 1 < rg.tiles) fetch_ids(tile + 1);
+        if (it >= S::stages) ok = tc::mbar_wait(empty_bar(st), ((it / S::stages) + 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv, kss = vst + S::kv, vss = kss + S::scales;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int n = min(32, mine - b * 32);
+          if (n <= 0) break;
+          const int first = pw * mine + b * 32;                       // tile-relative token of lane 0
+          const int tok = rg.t0 + tile * tile_tokens + first + lane;
+          bool valid = lane < n && tok < rg.t1;
+          if (valid && (unsigned)id[b] >= (unsigned)a.num_pages) {
+            report(a.status, SKV_DEV_PAGE_OOB);
+            valid = false;
+          }
+          const int64_t page = valid ? id[b] : 0;
+          const int slot = valid ? tok % a.page_size : 0, blk = slot / a.block_tokens;
+          const int64_t ko = valid ? page * a.k0 + slot * a.k1 : -1;  // -1: zero-filled
+          const int64_t vo = page * a.v0 + slot * a.v1;
+          const int64_t kso = page * a.ks0 + blk * a.ks1, vso = page * a.vs0 + blk * a.vs1;
+          const int copies = (n << a.hc_log2) * kChunks;              // a multiple of 32
+#pragma unroll 4
+          for (int x = lane; x < copies; x += 32) {
+            const int row = x / kChunks, c = x % kChunks, tl = row >> a.hc_log2, h = row & (hc - 1);
+            const int64_t kx = __shfl_sync(0xffffffffu, ko, tl), vx = __shfl_sync(0xffffffffu, vo, tl);
+            const int rt = first + tl;
+            const uint32_t dst = (uint32_t)((h * tile_tokens + rt) * D + ((c ^ swizzle<D>(rt)) << 4));
+            cp16(kst + dst, a.k + (kx < 0 ? 0 : kx + (int64_t)(h0 + h) * a.k2 + c * 16), kx >= 0);
+            cp16(vst + dst, a.v + (kx < 0 ? 0 : vx + (int64_t)(h0 + h) * a.v2 + c * 16), kx >= 0);
+          }
+          const int pairs = n << a.hc_log2;
+          for (int x0 = 0; x0 < pairs; x0 += 32) {
+            const int x = x0 + lane, tl = x >> a.hc_log2, h = x & (hc - 1);
+            const int64_t kx = __shfl_sync(0xffffffffu, ko, tl & 31);
+            const int64_t sk = __shfl_sync(0xffffffffu, kso, tl & 31), sv = __shfl_sync(0xffffffffu, vso, tl & 31);
+            if (x < pairs) {
+              const uint32_t dst = (uint32_t)((h * tile_tokens + first + tl) * 4);
+              cp4(kss + dst, a.ks + (kx < 0 ? 0 : sk + (int64_t)(h0 + h) * a.ks2), kx >= 0);
+              cp4(vss + dst, a.vs + (kx < 0 ? 0 : sv + (int64_t)(h0 + h) * a.vs2), kx >= 0);
+            }
+          }
+        }
+        cp_arrive(full_bar(st));
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+
+  // ================================================================================== consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int h = warp & (hc - 1), sub = warp >> a.hc_log2, subs = kConsumers >> a.hc_log2;
+  const int kh = h0 + h;
+  constexpr int kKSteps = D / 16;      // k-steps of Q . K^T
+  constexpr int kDims = D / 8;         // dims of O each lane column covers (n-tiles of P . V)
+  constexpr int kRowSets = WIDE ? 2 : 1;
+  int it = 0;
+  bool ok = true;
+  for (int wi = w_begin; wi < w_end; ++wi) {
+    const WorkItem w = a.work[wi];
+    const Range rg = item_range(a, w, tile_tokens);
+    const int rows = w.q_count * a.g - row0;
+    // rows g and g + 8 of the tile: query token, head, key limit
+    int qi[2], qh[2], limit[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int r = g + 8 * s, rr = min(r, max(rows - 1, 0)) + row0;
+      qi[s] = rr / a.g;
+      qh[s] = kh * a.g + rr - qi[s] * a.g;
+      limit[s] = min(rg.t1, w.split + qi[s]);
+    }
+    // every row of the warp sees keys below this one
+    int all_see = min(limit[0], limit[1]);
+#pragma unroll
+    for (int x = 16; x >= 4; x >>= 1) all_see = min(all_see, __shfl_xor_sync(0xffffffffu, all_see, x));
+
+    // Q in f16 under the k permutation: k-step 4 j + s of chunk j holds dims 16 (4 j + t) + 4 s ..
+    uint32_t qf[kKSteps][4];
+    float sc[2];
+    {
+      float x[2][D / 4];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const bool live = (WIDE || s == 0) && g + 8 * s < rows;
+        const __nv_bfloat16* src = a.q + ((int64_t)(w.q_start + qi[s]) * a.hq + qh[s]) * D;
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (live) v = __ldg(reinterpret_cast<const uint4*>(src + (4 * j + t) * 16 + e * 8));
+            const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[s][j * 16 + e * 8 + 2 * i] = bf16_lo(wd[i]);
+              x[s][j * 16 + e * 8 + 2 * i + 1] = bf16_hi(wd[i]);
+              mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(wd[i])), fabsf(bf16_hi(wd[i]))));
+            }
+          }
+        mx = quad_max(mx);
+        const int e = mx > 0.f ? max((int)(__float_as_uint(mx) >> 23) - 127, -100) : 14;
+        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        sc[s] = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[s][i] *= up;
+      }
+#pragma unroll
+      for (int ks = 0; ks < kKSteps; ++ks) {
+        const int i = (ks >> 2) * 16 + (ks & 3) * 4;
+        qf[ks][0] = pack_f16(x[0][i], x[0][i + 1]);
+        qf[ks][1] = WIDE ? pack_f16(x[1][i], x[1][i + 1]) : 0u;
+        qf[ks][2] = pack_f16(x[0][i + 2], x[0][i + 3]);
+        qf[ks][3] = WIDE ? pack_f16(x[1][i + 2], x[1][i + 3]) : 0u;
+      }
+    }
+
+    float o[kDims][2 * kRowSets];  // [dim of the lane's run][row set x (column 2t, 2t + 1)]
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < kDims; ++j)
+#pragma unroll
+      for (int x = 0; x < 2 * kRowSets; ++x) o[j][x] = 0.f;
+
+    for (int tile = 0; tile < rg.tiles; ++tile, ++it) {
+      const int st = it % S::stages;
+      ok = tc::mbar_wait(full_bar(st), (it / S::stages) & 1, abort_flag, a.status) && ok;
+      const int tb = rg.t0 + tile * tile_tokens + sub * kWarpTokens;  // first token of this warp
+      if (ok && tb < rg.t1) {
+        const int rt0 = sub * kWarpTokens;
+        const uint32_t kst = sbase + st * S::stage + (uint32_t)((h * tile_tokens + rt0) * D), vst = kst + S::kv;
+        const uint32_t kss = sbase + st * S::stage + 2 * S::kv + (uint32_t)((h * tile_tokens + rt0) * 4);
+        const uint32_t vss = kss + S::scales;
+        // ---- scores: 4 tiles of 8 tokens
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+          const int tok = 8 * n + col_token<D>(g);
+          const uint32_t row = kst + tok * D;
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 kw = lds128(row + (((4 * j + t) ^ swizzle<D>(tok)) << 4));
+            const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t b0, b1;
+              widen<I8>(wd[x], b0, b1);
+              mma16816(s[n], qf[4 * j + x], b0, b1);
+            }
+          }
+        }
+        // ---- scale, mask, maximum
+        const int ta = col_token<D>(2 * t), tc1 = col_token<D>(2 * t + 1);
+        float vsc[4][2];
+        float mx[2] = {-INFINITY, -INFINITY}, vref = 0.f;
+        const bool masked = tb + kWarpTokens > all_see;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float k0 = lds_f(kss + (8 * n + ta) * 4), k1 = lds_f(kss + (8 * n + tc1) * 4);
+          vsc[n][0] = lds_f(vss + (8 * n + ta) * 4);
+          vsc[n][1] = lds_f(vss + (8 * n + tc1) * 4);
+          vref = fmaxf(vref, fmaxf(vsc[n][0], vsc[n][1]));
+#pragma unroll
+          for (int r = 0; r < kRowSets; ++r) {
+            s[n][2 * r] *= k0 * sc[r];
+            s[n][2 * r + 1] *= k1 * sc[r];
+            if (masked) {
+              if (tb + 8 * n + ta >= limit[r]) s[n][2 * r] = -INFINITY;
+              if (tb + 8 * n + tc1 >= limit[r]) s[n][2 * r + 1] = -INFINITY;
+            }
+            mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
+          }
+        }
+        vref = quad_max(vref);
+        const float rv = vref > 0.f ? 1.f / vref : 0.f;
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < kRowSets; ++r) {
+          mx[r] = quad_max(mx[r]);
+          raise |= mx[r] > m[r] + kRaise;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int r = 0; r < kRowSets; ++r) {
+            const float mn = mx[r] > m[r] + kRaise ? mx[r] : m[r];
+            const float al = mn == m[r] ? 1.f : ex2f(m[r] - mn);
+            l[r] *= al;
+            m[r] = mn;
+#pragma unroll
+            for (int j = 0; j < kDims; ++j) {
+              o[j][2 * r] *= al;
+              o[j][2 * r + 1] *= al;
+            }
+          }
+        }
+        // ---- weights
+        uint32_t pf[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if (r < kRowSets) {
+              const float mm = m[r] == -INFINITY ? 0.f : m[r];
+              const float p0 = ex2f(s[n][2 * r] - mm), p1 = ex2f(s[n][2 * r + 1] - mm);
+              l[r] += p0 + p1;
+              pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * (vsc[n][0] * rv), p1 * (vsc[n][1] * rv));
+            } else {
+              pf[n >> 1][(n & 1) * 2 + r] = 0u;
+            }
+          }
+        }
+        // ---- O += P . V: per lane 16 (D = 128) or 8 dims of 8 tokens
+        constexpr int kWords = D / 32;  // words of a lane's run of dims
+        uint32_t vw[4][2][kWords];      // [8-token group][token of the pair][word]
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int tok = 8 * n + (e ? tc1 : ta);
+            const uint32_t row = vst + tok * D;
+            if constexpr (D == 128) {
+              const uint4 v = lds128(row + ((col_token<D>(g) ^ swizzle<D>(tok)) << 4));
+              vw[n][e][0] = v.x;
+              vw[n][e][1] = v.y;
+              vw[n][e][2] = v.z;
+              vw[n][e][3] = v.w;
+            } else {
+              const uint2 v = lds64(row + (((g >> 1) ^ swizzle<D>(tok)) << 4) + ((g & 1) << 3));
+              vw[n][e][0] = v.x;
+              vw[n][e][1] = v.y;
+            }
+          }
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+          uint32_t b[4][4];  // [8-token group][dim]: pairs of tokens
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            widen<I8>(__byte_perm(vw[n][0][q], vw[n][1][q], 0x5140), b[n][0], b[n][1]);
+            widen<I8>(__byte_perm(vw[n][0][q], vw[n][1][q], 0x7362), b[n][2], b[n][3]);
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(c, pf[0], b[0][d], b[1][d]);
+            mma16816(c, pf[1], b[2][d], b[3][d]);
+#pragma unroll
+            for (int x = 0; x < 2 * kRowSets; ++x) o[4 * q + d][x] = fmaf(c[x], vref, o[4 * q + d][x]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(empty_bar(st));
+    }
+#pragma unroll
+    for (int r = 0; r < kRowSets; ++r) l[r] = quad_sum(l[r]);
+
+    // ---- join the warps of a head: half of them hand over to the other half, until one is left
+    float* mbuf = reinterpret_cast<float*>(smem + S::merge);
+    float2* sbuf = reinterpret_cast<float2*>(smem + S::stat);
+    for (int half = subs >> 1; half > 0; half >>= 1) {
+      const bool gives = sub >= half && sub < 2 * half, takes = sub < half;
+      const int place = (sub - (gives ? half : 0)) * hc + h;  // < 4
+#pragma unroll
+      for (int r = 0; r < kRowSets; ++r) {
+        tc::named_bar_sync(1, 32 * kConsumers);
+        float4* mine = reinterpret_cast<float4*>(mbuf + place * 8 * D) + lane;
+        if (gives) {
+          if (t == 0) sbuf[place * 16 + 8 * r + g] = make_float2(m[r], l[r]);
+#pragma unroll
+          for (int j = 0; j < kDims; j += 2)
+            mine[(j >> 1) * 32] = make_float4(o[j][2 * r], o[j][2 * r + 1], o[j + 1][2 * r], o[j + 1][2 * r + 1]);
+        }
+        tc::named_bar_sync(1, 32 * kConsumers);
+        if (takes) {
+          const float2 ml = sbuf[place * 16 + 8 * r + g];
+          const float mn = fmaxf(m[r], ml.x), base = mn == -INFINITY ? 0.f : mn;
+          const float fa = ex2f(m[r] - base), fb = ex2f(ml.x - base);
+          m[r] = mn;
+          l[r] = l[r] * fa + ml.y * fb;
+#pragma unroll
+          for (int j = 0; j < kDims; j += 2) {
+            const float4 x = mine[(j >> 1) * 32];
+            o[j][2 * r] = o[j][2 * r] * fa + x.x * fb;
+            o[j][2 * r + 1] = o[j][2 * r + 1] * fa + x.y * fb;
+            o[j + 1][2 * r] = o[j + 1][2 * r] * fa + x.z * fb;
+            o[j + 1][2 * r + 1] = o[j + 1][2 * r + 1] * fa + x.w * fb;
+          }
+        }
+      }
+    }
+    if (sub != 0) continue;
+    // ---- write: column 2t holds dims d0 .., column 2t + 1 dims d1 .. of the rows
+    const int d0 = D == 128 ? 16 * t : 16 * t, d1 = D == 128 ? 64 + 16 * t : 16 * t + 8;
+#pragma unroll
+    for (int r = 0; r < kRowSets; ++r) {
+      if (g + 8 * r >= rows) continue;
+      const float inv = l[r] > 0.f || l[r] != l[r] ? 1.f / l[r] : 0.f;
+      const float lse = l[r] > 0.f || l[r] != l[r] ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+      if (w.part_row < 0) {
+        const int64_t at = (int64_t)(w.q_start + qi[r]) * a.hq + qh[r];
+        if (t == 0 && a.lse != nullptr) a.lse[at] = lse;
+        OutT* dst = reinterpret_cast<OutT*>(a.o) + at * D;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < kDims; j += 8) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = o[j + e][2 * r + c] * inv;
+            OutT* p = dst + (c ? d1 : d0) + j;
+            if constexpr (sizeof(OutT) == 4) {
+              reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+              reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+              uint4 u;
+              __nv_bfloat162 h2[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) h2[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+              u.x = *reinterpret_cast<uint32_t*>(&h2[0]);
+              u.y = *reinterpret_cast<uint32_t*>(&h2[1]);
+              u.z = *reinterpret_cast<uint32_t*>(&h2[2]);
+              u.w = *reinterpret_cast<uint32_t*>(&h2[3]);
+              *reinterpret_cast<uint4*>(p) = u;
+            }
+          }
+      } else {
+        const int64_t at = ((int64_t)w.part_row + (int64_t)qi[r] * w.part_stride) * a.hq + qh[r];
+        if (t == 0) a.lse_part[at] = lse;
+        float* dst = a.o_part + at * D;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < kDims; j += 4)
+            *reinterpret_cast<float4*>(dst + (c ? d1 : d0) + j) =
+                make_float4(o[j][2 * r + c] * inv, o[j + 1][2 * r + c] * inv, o[j + 2][2 * r + c] * inv,
+                            o[j + 3][2 * r + c] * inv);
+      }
+    }
+  }
+}
+
+template <bool I8, int D, bool WIDE, typename OutT>
+int launch_s(const SArgs& a, int ctas, cudaStream_t s) {
+  static DeviceSmemAttr attr;
+  const int smem = Smem<D>::total;
+  if (const int e = attr.ensure(reinterpret_cast<const void*>(gqa_scaled_kernel<I8, D, WIDE, OutT>), smem)) return e;
+  gqa_scaled_kernel<I8, D, WIDE, OutT><<<ctas * a.head_groups * a.row_groups, kThreads, smem, s>>>(a);
+  return (int)cudaGetLastError();
+}
+template <bool I8, int D, bool WIDE>
+int launch_o(const SArgs& a, int ctas, int o_dtype, cudaStream_t s) {
+  return o_dtype == SKV_BF16 ? launch_s<I8, D, WIDE, __nv_bfloat16>(a, ctas, s) : launch_s<I8, D, WIDE, float>(a, ctas, s);
+}
+template <bool I8>
+int launch_d(const SArgs& a, int ctas, int head_dim, bool wide, int o_dtype, cudaStream_t s) {
+  if (head_dim == 128) return wide ? launch_o<I8, 128, true>(a, ctas, o_dtype, s) : launch_o<I8, 128, false>(a, ctas, o_dtype, s);
+  return wide ? launch_o<I8, 64, true>(a, ctas, o_dtype, s) : launch_o<I8, 64, false>(a, ctas, o_dtype, s);
+}
+
+}  // namespace
+
+// Rows of one tile are (query token, head of the group): 8 when a request's rows fit, else 16; a
+// group of more than 16 heads is cut into row groups that run as CTAs side by side.
+int gqa_scaled_q_tile(int group, int max_q_len) {
+  const int rows = (int64_t)group * max_q_len <= 8 ? 8 : 16;
+  return std::max(1, rows / group);
+}
+int gqa_scaled_units(int num_kv_heads, int group) {
+  int hc = 8;
+  while (num_kv_heads % hc) hc >>= 1;
+  return num_kv_heads / hc * ((group + 15) / 16);
+}
+int gqa_scaled_tile_tokens(int num_kv_heads) {
+  int hc = 8;
+  while (num_kv_heads % hc) hc >>= 1;
+  return kConsumers * kWarpTokens / hc;
+}
+
+int launch_gqa_scaled(const skv_paged_scaled_params& sp, const WorkItem* work, const int32_t* cta_indptr, int num_ctas,
+                      int q_tile, cudaStream_t s) {
+  const skv_paged_params& p = sp.base;
+  SArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(p.q);
+  a.k = static_cast<const uint8_t*>(p.k_cache);
+  a.v = static_cast<const uint8_t*>(p.v_cache);
+  a.ks = sp.k_scale;
+  a.vs = sp.v_scale;
+  a.k0 = p.k_stride[0];
+  a.k1 = p.k_stride[1];
+  a.k2 = p.k_stride[2];
+  a.v0 = p.v_stride[0];
+  a.v1 = p.v_stride[1];
+  a.v2 = p.v_stride[2];
+  a.ks0 = sp.k_scale_stride[0];
+  a.ks1 = sp.k_scale_stride[1];
+  a.ks2 = sp.k_scale_stride[2];
+  a.vs0 = sp.v_scale_stride[0];
+  a.vs1 = sp.v_scale_stride[1];
+  a.vs2 = sp.v_scale_stride[2];
+  a.kv_indptr = p.kv_indptr;
+  a.kv_indices = p.kv_indices;
+  a.last = p.kv_last_page_len;
+  a.work = work;
+  a.cta_indptr = cta_indptr;
+  a.num_pages = p.num_pages;
+  a.page_size = p.page_size;
+  a.block_tokens = sp.block_tokens;
+  a.hq = p.num_qo_heads;
+  a.hk = p.num_kv_heads;
+  a.g = p.num_qo_heads / p.num_kv_heads;
+  a.hc_log2 = 3;
+  while (a.hk % (1 << a.hc_log2)) --a.hc_log2;
+  a.head_groups = a.hk >> a.hc_log2;
+  a.row_groups = (a.g + 15) / 16;
+  a.scale_log2 = p.sm_scale * kLog2e;
+  a.o = p.o;
+  a.lse = p.lse;
+  a.o_part = p.o_part;
+  a.lse_part = p.lse_part;
+  a.status = p.status;
+  const bool wide = q_tile * a.g > 8;
+  return p.kv_dtype == SKV_I8 ? launch_d<true>(a, num_ctas, p.head_dim, wide, p.o_dtype, s)
+                              : launch_d<false>(a, num_ctas, p.head_dim, wide, p.o_dtype, s);
+}
+
+}  // namespace skv

@@ -30,6 +30,7 @@ enum KernelId : int32_t {
   KERNEL_GQA_TC_DECODE = 2,
   KERNEL_GQA_TC_WIDE = 3,
   KERNEL_GQA_TC_PREFILL = 4,  // tensor-core, 128 query rows (tokens x group heads) per unit
+  KERNEL_GQA_SCALED = 5,      // 8-bit cache with block scales, 8 or 16 query rows per tile
   KERNEL_MLA_SIMT = 11,
   KERNEL_MLA_TC16 = 12,  // tensor-core MLA, 16 query rows per unit (bf16 or e4m3 cache)
   KERNEL_MLA_TC32 = 13,  // tensor-core MLA, 32 query rows per unit (bf16 or e4m3 cache)
@@ -121,6 +122,11 @@ int launch_merge(const float* o_states, const float* lse_states, const int32_t* 
                  int32_t num_states, const MergeItem* items, int64_t num_rows, int32_t num_heads,
                  int32_t head_dim, void* o_out, int32_t o_dtype, float* lse_out, cudaStream_t s);
 int launch_splice(const skv_splice_params& p, const skv_splice_chunk* chunks, int num_chunks, cudaStream_t s);
+int gqa_scaled_q_tile(int group, int max_q_len);  // query tokens of a tile
+int gqa_scaled_units(int num_kv_heads, int group);  // CTAs that share a KV slice (head and row groups)
+int gqa_scaled_tile_tokens(int num_kv_heads);
+int launch_gqa_scaled(const skv_paged_scaled_params& p, const WorkItem* work, const int32_t* cta_indptr, int num_ctas,
+                      int q_tile, cudaStream_t s);
 int launch_rope(const skv_rope_params& p, cudaStream_t s);
 int launch_kv_append(const skv_append_params& p, cudaStream_t s);
 int launch_gather(const skv_paged_params& p, const int32_t* token_indptr, int64_t total_tokens,

@@ -8,8 +8,9 @@ from typing import Optional
 
 import numpy as np
 
-from . import (AppendParams, BF16, E4M3, F32, I8, Rope, RopeParams, _check, _index_ptr, _kv_append, _ROPE,
-               _ROPE_SCALING, _rope_apply, _rope_frequencies)
+from . import (AppendParams, BF16, E4M3, F32, I8, PagedParams, PagedScaledParams, Plan, Rope, RopeParams, _check,
+               _index_ptr, _kv_append, _ROPE, _ROPE_SCALING, _rope_apply, _rope_frequencies, _scaled_fwd,
+               plan_paged_scaled)
 
 _NULL = nullcontext()
 
@@ -206,3 +207,72 @@ def paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices
         _check(_kv_append(ctypes.byref(p), _stream(stream, dev)), "skv_paged_kv_append")
     del keep
     return q_out
+
+
+def _dev_i32(a, dev):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype=np.int32))).to(dev)
+
+
+def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, kv_indptr_h, kv_indices,
+                           kv_last_page_len_h, *, sm_scale: Optional[float] = None, causal: bool = False,
+                           policy="balanced", param: int = 0, split_page_start=None, o_dtype=None,
+                           num_pages: Optional[int] = None, kv_indptr=None, kv_last_page_len=None,
+                           plan: Optional[Plan] = None, status=None, stream=None, o_out=None, lse_out=None):
+    """GQA attention over a paged 8-bit cache with block scales (skv_paged_attn_scaled_fwd): q [total_q, Hq, D]
+    bf16, caches [num_pages, P, Hk, D] float8_e4m3fn or int8, ``k_scale`` / ``v_scale`` float32
+    [num_pages, P / block, Hk], as ``paged_kv_append`` writes them.  ``causal``: a request's query tokens are
+    its last positions and each sees keys up to its own.  Host page-table shape arrays (``*_h``) feed
+    the planner; ``plan`` (``plan_paged_scaled`` with the same ``causal``) and device copies ``kv_indptr`` /
+    ``kv_last_page_len`` may be kept over the layers of a step.
+    Returns (o, lse, extras) with extras = {"plan", "o_part", "lse_part"}."""
+    import torch
+    _need(q.dim() == 3 and k_cache.dim() == 4, "q is [total_q, Hq, D], the caches [num_pages, P, Hk, D]")
+    dev, total_q, hq, dim = q.device, q.shape[0], q.shape[1], q.shape[2]
+    hk, page = k_cache.shape[2], k_cache.shape[1]
+    code = _cache_code(k_cache.dtype)
+    _need(q.dtype == torch.bfloat16 and q.is_contiguous(), "q must be contiguous bfloat16")
+    _need(code in (E4M3, I8) and v_cache.dtype == k_cache.dtype, "caches must both be float8_e4m3fn or int8")
+    _need(v_cache.shape == k_cache.shape and k_cache.shape[3] == dim and k_cache.stride(3) == 1
+          and v_cache.stride(3) == 1, "the caches must be [num_pages, P, Hk, D] with the head_dim of q")
+    _need(len(qo_indptr_h) > 0 and total_q >= int(qo_indptr_h[-1]), "q has fewer rows than qo_indptr names")
+    pages = k_cache.shape[0] if num_pages is None else num_pages
+    _need(0 <= pages <= k_cache.shape[0], "num_pages is more than the cache holds")
+    block = _scales(k_cache, k_scale, v_scale, pages)
+    batch = len(qo_indptr_h) - 1
+    _on(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, kv_indices=kv_indices,
+        kv_indptr=kv_indptr, kv_last_page_len=kv_last_page_len, status=status, o_out=o_out, lse_out=lse_out)
+    _index("kv_indices", kv_indices)
+    _index("kv_indptr", kv_indptr, batch + 1)
+    _index("kv_last_page_len", kv_last_page_len, batch)
+    for name, t, shape in (("o_out", o_out, (total_q, hq, dim)), ("lse_out", lse_out, (total_q, hq))):
+        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous()), f"{name} must be contiguous {shape}")
+    _need(lse_out is None or lse_out.dtype == torch.float32, "lse_out must be float32")
+    out_dtype = o_out.dtype if o_out is not None else (o_dtype or torch.float32)
+    _need(out_dtype in (torch.float32, torch.bfloat16), "outputs are float32 or bfloat16")
+    with _device(dev), _on_stream(stream, dev):
+        if plan is None:
+            plan = plan_paged_scaled(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, page, hq, hk, dim, causal, policy,
+                                     param, split_page_start)
+        if plan.device is None:
+            plan.to(dev)
+        if kv_indptr is None:
+            kv_indptr = _dev_i32(kv_indptr_h, dev)
+        if kv_last_page_len is None:
+            kv_last_page_len = _dev_i32(kv_last_page_len_h, dev)
+        o = torch.empty(total_q, hq, dim, dtype=out_dtype, device=dev) if o_out is None else o_out
+        lse = torch.empty(total_q, hq, dtype=torch.float32, device=dev) if lse_out is None else lse_out
+        n_part = plan.info.num_partial_rows
+        o_part = torch.empty(n_part, hq, dim, dtype=torch.float32, device=dev) if n_part else None
+        lse_part = torch.empty(n_part, hq, dtype=torch.float32, device=dev) if n_part else None
+        base = PagedParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride()[:3],
+                           v_cache.stride()[:3], kv_indptr.data_ptr(), _index_ptr(kv_indices),
+                           _index_ptr(kv_last_page_len), batch, total_q, pages, page, hq, hk, dim,
+                           dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(),
+                           BF16 if out_dtype == torch.bfloat16 else F32, lse.data_ptr(),
+                           o_part.data_ptr() if n_part else None, lse_part.data_ptr() if n_part else None,
+                           None if status is None else status.data_ptr(), code, 1.0)
+        p = PagedScaledParams(base, k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(), v_scale.stride(), block)
+        _check(_scaled_fwd(ctypes.byref(p), plan.device.data_ptr(), ctypes.byref(plan.info), _stream(stream, dev)),
+               "skv_paged_attn_scaled_fwd")
+    return o, lse, {"plan": plan, "o_part": o_part, "lse_part": lse_part}

@@ -178,3 +178,84 @@ def test_struct_layouts():
     got, want = c_layout([(skv.Rope, "skv_rope"), (skv.RopeParams, "skv_rope_params"),
                           (skv.AppendParams, "skv_append_params")])
     assert got == want
+
+
+def _plan_scaled(**kw):
+    a = dict(batch=2, qo=[0, 1, 2], kv=[0, 3, 5], last=[4, 16], page=16, hq=8, hk=2, d=64, causal=0, policy=0, param=0)
+    a.update(kw)
+    arrays = [None if a[k] is None else np.asarray(a[k], dtype=np.int32) for k in ("qo", "kv", "last")]
+    info, plan = skv.PlanInfo(), np.zeros(4096, np.int32)
+    code = skv._plan_scaled(a["batch"], *[skv._ptr_i32(x) for x in arrays], a["page"], a["hq"], a["hk"], a["d"],
+                            a["causal"], a["policy"], a["param"], None, None, skv._ptr_i32(plan), plan.size,
+                            ctypes.byref(info))
+    return code, plan, info
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(), skv.OK), (dict(batch=-1), skv.ERR_INVALID), (dict(qo=None), skv.ERR_INVALID), (dict(kv=None), skv.ERR_INVALID),
+    (dict(qo=[1, 2, 3]), skv.ERR_INVALID), (dict(qo=[0, 2, 1]), skv.ERR_INVALID), (dict(kv=[0, 3, 2]), skv.ERR_INVALID),
+    (dict(last=[17, 1]), skv.ERR_INVALID), (dict(hq=7), skv.ERR_INVALID), (dict(hk=0), skv.ERR_INVALID),
+    (dict(d=96), skv.ERR_UNSUPPORTED), (dict(policy=9), skv.ERR_INVALID), (dict(policy=1, param=0), skv.ERR_INVALID),
+    (dict(hq=131072, hk=65536), skv.ERR_UNSUPPORTED), (dict(page=0), skv.ERR_INVALID),
+])
+def test_plan_scaled_refusals(change, code):
+    assert _plan_scaled(**change)[0] == code
+
+
+@pytest.mark.parametrize("hq,hk,q_len,tile", [(8, 8, 1, 8), (64, 8, 1, 1), (32, 8, 4, 4), (64, 8, 4, 2), (40, 2, 3, 1),
+                                              (6, 2, 9, 5), (24, 1, 2, 1)])
+def test_plan_scaled_items(hq, hk, q_len, tile):
+    """Every (query token, key page) of a request is in one item; causal limits count from the item's first token."""
+    for causal in (0, 1):
+        code, plan, info = _plan_scaled(qo=[0, q_len, 2 * q_len], hq=hq, hk=hk, causal=causal, policy=2, param=148)
+        assert code == skv.OK and info.kernel == 5 and info.q_tile == tile
+        seen = np.zeros((2 * q_len, 5), int)
+        for r, q0, n, p0, p1, _, _, limit in plan[:8 * info.num_work].reshape(-1, 8):
+            assert n <= tile
+            seen[q0:q0 + n, [0, 3][r] + p0:[0, 3][r] + p1] += 1
+            assert limit == ([36, 32][r] - q_len + q0 - r * q_len + 1 if causal else 1 << 30)
+        assert np.all(seen[:q_len, :3] == 1) and np.all(seen[q_len:, 3:] == 1) and seen.sum() == 5 * q_len
+
+
+def _scaled_params(**kw):
+    base = dict(q=PTR, k_cache=PTR, v_cache=PTR, k_stride=(2048, 128, 64), v_stride=(2048, 128, 64), kv_indptr=PTR,
+                kv_indices=PTR, kv_last_page_len=PTR, batch=2, total_q=2, num_pages=5, page_size=16, num_qo_heads=8,
+                num_kv_heads=2, head_dim=64, sm_scale=0.1, o=PTR, o_dtype=skv.F32, lse=PTR, o_part=PTR, lse_part=PTR,
+                status=None, kv_dtype=skv.I8, kv_scale=1.0)
+    top = dict(k_scale=PTR, v_scale=PTR, k_scale_stride=(2, 2, 1), v_scale_stride=(2, 2, 1), block_tokens=16)
+    for k, v in kw.items():
+        (base if k in base else top)[k] = v
+    return skv.PagedScaledParams(base=skv.PagedParams(**base), **top)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(kv_dtype=skv.BF16), skv.ERR_UNSUPPORTED), (dict(head_dim=32), skv.ERR_UNSUPPORTED),
+    (dict(num_qo_heads=7), skv.ERR_INVALID), (dict(o_dtype=skv.E4M3), skv.ERR_UNSUPPORTED),
+    (dict(block_tokens=0), skv.ERR_INVALID), (dict(block_tokens=5), skv.ERR_INVALID), (dict(q=None), skv.ERR_INVALID),
+    (dict(k_scale=None), skv.ERR_INVALID), (dict(v_scale_stride=(-2, 2, 1)), skv.ERR_INVALID),
+    (dict(k_stride=(2048, 128, 72)), skv.ERR_ALIGNMENT), (dict(v_stride=(-2048, 128, 64)), skv.ERR_INVALID),
+    (dict(v_cache=PTR + 8), skv.ERR_ALIGNMENT), (dict(q=PTR + 2), skv.ERR_ALIGNMENT),
+    (dict(o_part=None), skv.ERR_WORKSPACE), (dict(kv_indices=None), skv.ERR_INVALID), (dict(batch=-1), skv.ERR_INVALID),
+    (dict(num_qo_heads=64), skv.ERR_INVALID),           # a plan for another group
+])
+def test_scaled_fwd_refusals(change, code):
+    _, plan, info = _plan_scaled(qo=[0, 4, 8], policy=1, param=2)
+    assert info.num_partial_rows > 0
+    p = _scaled_params(**change)
+    assert skv._scaled_fwd(ctypes.byref(p), PTR, ctypes.byref(info), None) == code
+
+
+def test_plans_run_only_on_their_own_call():
+    _, _, info = _plan_scaled()
+    assert skv._paged_fwd(ctypes.byref(_scaled_params(kv_dtype=skv.BF16).base), PTR, ctypes.byref(info), None) == skv.ERR_INVALID
+    other = skv.plan_paged([0, 1, 2], [0, 3, 5], [4, 16], 16, 8, 2, 64, "none").info
+    assert skv._scaled_fwd(ctypes.byref(_scaled_params()), PTR, ctypes.byref(other), None) == skv.ERR_INVALID
+    assert skv._scaled_fwd(None, PTR, ctypes.byref(info), None) == skv.ERR_INVALID
+
+
+def test_scaled_struct_layout():
+    import shutil
+    if shutil.which("gcc") is None:
+        pytest.skip("needs a C compiler")
+    got, want = c_layout([(skv.PagedScaledParams, "skv_paged_scaled_params")])
+    assert got == want

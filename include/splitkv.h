@@ -27,6 +27,8 @@
  *   skv_paged_attn_scaled_fwd  GQA attention over a paged cache held in 8 bits (e4m3 or int8) with
  *                       one scale for each block of tokens and KV head, optionally causal among
  *                       a request's query tokens.
+ *   skv_prompt_attn_fwd Attention over whole prompts, packed and of different lengths, causal or not,
+ *                       keys and values as the projections left them (no page table).
  *   skv_rope_apply      Rotary positions of queries and keys (both pair layouts, part of the head,
  *                       frequencies stretched for long contexts by skv_rope_frequencies).
  *   skv_paged_kv_append New keys and values into the paged cache, rotated on the way; the cache
@@ -112,7 +114,7 @@ typedef struct {
                             /*   CUDA cores, 2 GQA tensor-core decode per KV head, 3 GQA      */
                             /*   tensor-core decode over all KV heads, 4 GQA tensor-core      */
                             /*   prefill (128 query rows), 5 GQA decode over a block-scaled   */
-                            /*   8-bit cache, 11 MLA on CUDA cores, 12 / 13 / 14 MLA tensor    */
+                            /*   8-bit cache, 6 packed prompts, 11 MLA on CUDA cores, 12 / 13 / 14 MLA tensor    */
                             /*   cores with 16 / 32 / 64 query rows per tile                  */
   int32_t q_tile;           /* query tokens per work item (MLA: the fold ratio F)             */
   int32_t plan_words;       /* int32 words of the plan actually used                          */
@@ -456,6 +458,50 @@ typedef struct {
 
 SKV_API skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* p, const int32_t* plan_d,
                                              const skv_plan_info* info, skv_stream_t stream);
+
+/* -------------------------------------------------------------------------------------------
+ * skv_plan_prompt / skv_prompt_attn_fwd -- attention over whole prompts, packed back to back.
+ *   Sequence r has query rows qo_indptr_h[r] .. qo_indptr_h[r+1] of q and key rows kv_indptr_h[r] ..
+ *   kv_indptr_h[r+1] of k and v (kv_indptr_h NULL: the same rows).  With `causal` its n query tokens
+ *   are the last n of its L positions and query token i sees keys t <= L - n + i (more keys than
+ *   query tokens: a prompt taken in chunks; fewer: the first tokens see none, O = 0, LSE = -inf).
+ *   Query head h reads KV head h / (Hq / Hk).  bf16 inputs with any (token, head) strides of whole
+ *   16 bytes, so q, k, v may be slices of one projection; head_dim 64 or 128; sm_scale > 0.
+ *   Rows of q behind the last sequence are not read, and those of o and lse left as they are.
+ *   Keys of other sequences never reach a result, NaN or not; a key that some query token of its
+ *   own sequence sees must have finite K and V (where it is masked for another token its weight is
+ *   0, and 0 x NaN is not 0).
+ *   `num_sms` (0: the current device's) is what the plan balances over; sequences with few query
+ *   tokens over many keys are cut along the keys, their partials go to o_part / lse_part
+ *   ([num_partial_rows, Hq, D] and [num_partial_rows, Hq]) and are merged on the same stream.
+ * ----------------------------------------------------------------------------------------- */
+SKV_API skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
+                                   int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t causal,
+                                   int32_t num_sms, int32_t* plan_h, int64_t plan_capacity, skv_plan_info* info);
+
+typedef struct {
+  const void* q;            /* bf16 [total_q, Hq, D]                                                */
+  const void* k;            /* bf16 [total_kv, Hk, D]                                               */
+  const void* v;
+  int64_t q_stride[2];      /* (token, head) strides in elements: multiples of 8, and > 0 where the   */
+  int64_t k_stride[2];      /*   dimension has more than one entry                                   */
+  int64_t v_stride[2];
+  int32_t total_q;          /* rows of q, o and lse                                                  */
+  int32_t total_kv;
+  int32_t num_qo_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  float sm_scale;           /* finite, > 0                                                           */
+  void* o;                  /* [total_q, Hq, D] contiguous, of o_dtype                                */
+  int32_t o_dtype;          /* SKV_F32 or SKV_BF16                                                    */
+  float* lse;               /* [total_q, Hq] (may be NULL)                                            */
+  float* o_part;            /* partials of a plan that cuts along the keys                             */
+  float* lse_part;
+  int32_t* status;          /* device status word (may be NULL)                                       */
+} skv_prompt_params;
+
+SKV_API skv_status skv_prompt_attn_fwd(const skv_prompt_params* p, const int32_t* plan_d,
+                                       const skv_plan_info* info, skv_stream_t stream);
 
 /* -------------------------------------------------------------------------------------------
  * Rotary positions.  Pair p of a head's first `dim` values turns by the angle

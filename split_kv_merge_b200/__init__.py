@@ -8,7 +8,7 @@ there is no fallback path.
 Functions mirror the C ABI in include/splitkv.h:
 ``plan_paged``, ``paged_attn_fwd``, ``pod_attn_fwd``, ``plan_mla``, ``mla_decode_fwd``, ``merge_states``,
 ``paged_kv_gather``, ``mla_splice``, ``rope_frequencies``, ``rope_apply``, ``paged_kv_append``,
-``plan_paged_scaled``, ``paged_attention_scaled``,
+``plan_paged_scaled``, ``paged_attention_scaled``, ``plan_prompt``, ``prompt_attention``,
 ``mla_fold_ratio``, ``status_str``, ``version``.
 """
 from __future__ import annotations
@@ -93,6 +93,14 @@ class PagedScaledParams(ctypes.Structure):
                 ("v_scale_stride", ctypes.c_int64 * 3), ("block_tokens", ctypes.c_int32)]
 
 
+class PromptParams(ctypes.Structure):
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("q_stride", ctypes.c_int64 * 2), ("k_stride", ctypes.c_int64 * 2),
+                ("v_stride", ctypes.c_int64 * 2), ("total_q", ctypes.c_int32), ("total_kv", ctypes.c_int32),
+                ("num_qo_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("sm_scale", ctypes.c_float), ("o", _vp), ("o_dtype", ctypes.c_int32), ("lse", _vp), ("o_part", _vp),
+                ("lse_part", _vp), ("status", _vp)]
+
+
 class Rope(ctypes.Structure):
     _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("theta", ctypes.c_double),
                 ("inv_freq_h", _vp), ("mscale", ctypes.c_float)]
@@ -165,6 +173,10 @@ _plan_scaled = _proto("skv_plan_paged_scaled", ctypes.c_int, [ctypes.c_int32, _i
                       [ctypes.c_int32] * 7 + [_i32p, _i32p, _i32p, ctypes.c_int64, ctypes.POINTER(PlanInfo)])
 _scaled_fwd = _proto("skv_paged_attn_scaled_fwd", ctypes.c_int, [ctypes.POINTER(PagedScaledParams), _vp,
                                                                  ctypes.POINTER(PlanInfo), _vp])
+_plan_prompt = _proto("skv_plan_prompt", ctypes.c_int, [ctypes.c_int32, _i32p, _i32p] + [ctypes.c_int32] * 5 +
+                      [_i32p, ctypes.c_int64, ctypes.POINTER(PlanInfo)])
+_prompt_fwd = _proto("skv_prompt_attn_fwd", ctypes.c_int, [ctypes.POINTER(PromptParams), _vp,
+                                                           ctypes.POINTER(PlanInfo), _vp])
 _rope_frequencies = _proto("skv_rope_frequencies", ctypes.c_int,
                            [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                             ctypes.c_double, ctypes.c_double, _vp, ctypes.POINTER(ctypes.c_float)])
@@ -180,7 +192,7 @@ SYMBOLS = ["skv_plan_paged", "skv_paged_attn_fwd", "skv_paged_attn_partial", "sk
            "skv_mla_fold_ratio", "skv_status_str", "skv_version", "skv_paged_attn_fwd_static_scratch",
            "skv_test_wait_timeout", "skv_mla_splice", "skv_causal_tables", "skv_plan_paged_subset",
            "skv_pod_attn_fwd", "skv_rope_frequencies", "skv_rope_apply", "skv_paged_kv_append",
-           "skv_plan_paged_scaled", "skv_paged_attn_scaled_fwd"]
+           "skv_plan_paged_scaled", "skv_paged_attn_scaled_fwd", "skv_plan_prompt", "skv_prompt_attn_fwd"]
 
 
 class SkvError(RuntimeError):
@@ -338,6 +350,23 @@ def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, nu
     return _plan(_plan_scaled, lambda pol: (b, _ptr_i32(qo), _ptr_i32(ki), _ptr_i32(la), page_size, num_qo_heads,
                                             num_kv_heads, head_dim, int(causal), pol, param),
                  policy, split_page_start, "skv_plan_paged_scaled")
+
+
+def plan_prompt(qo_indptr, kv_indptr, num_qo_heads: int, num_kv_heads: int, head_dim: int, causal: bool = True,
+                num_sms: int = 0) -> Plan:
+    """Host planner (skv_plan_prompt) for packed prompts; ``kv_indptr`` None: keys are the queries' rows."""
+    qo = _i32(qo_indptr)
+    ki = None if kv_indptr is None else _i32(kv_indptr)
+    if ki is not None and len(ki) != len(qo):
+        raise ValueError("qo_indptr and kv_indptr must name the same sequences")
+    info = PlanInfo()
+    args = (len(qo) - 1, _ptr_i32(qo), _ptr_i32(ki), num_qo_heads, num_kv_heads, head_dim, int(causal), num_sms)
+    code = _plan_prompt(*args, None, 0, ctypes.byref(info))
+    if code not in (OK, ERR_WORKSPACE):
+        _check(code, "skv_plan_prompt")
+    words = np.zeros(max(1, info.plan_words), dtype=np.int32)
+    _check(_plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info)), "skv_plan_prompt")
+    return Plan(words[: info.plan_words] if info.plan_words else words[:0], info)
 
 
 # ----------------------------------------------------------------------------- launches
@@ -547,6 +576,7 @@ def library_path() -> str:
     return _LIB_PATH
 
 
-from .serving import (paged_attention_scaled, paged_kv_append, rope_apply, rope_frequencies)  # noqa: E402,F401
+from .serving import (paged_attention_scaled, paged_kv_append, prompt_attention, rope_apply,  # noqa: E402,F401
+                      rope_frequencies)
 from .runner import (CausalMlaDecode, PagedDecodePipeline, PodAttention, RouteMerge, mla_decode,  # noqa: E402,F401
                      paged_attention, pod_attention, pod_decode_sms)

@@ -1,9 +1,15 @@
-// C ABI of the serving operators around the attention calls: rotary positions and the cache
-// append.  Argument checks only; the work is in rope.cu and kv_append.cu.
+// C ABI of the serving operators around the paged attention calls: rotary positions, the cache
+// append and packed prompt attention.  Argument checks and the prompt planner; the work is in
+// rope.cu, kv_append.cu and prompt_attn.cu.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <cstring>
+#include <queue>
+#include <vector>
 
+#include "prompt_plan.h"
 #include "rope.cuh"
 
 using namespace skv;
@@ -149,6 +155,166 @@ skv_status skv_paged_kv_append(const skv_append_params* p, skv_stream_t stream) 
     if (st != SKV_OK) return st;
   }
   return cuda_status(launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
+                           int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t causal,
+                           int32_t num_sms, int32_t* plan_h, int64_t plan_capacity, skv_plan_info* info) try {
+  if (info == nullptr) return SKV_ERR_INVALID;
+  std::memset(info, 0, sizeof(*info));
+  if (batch < 0 || qo_indptr_h == nullptr || num_qo_heads < 1 || num_kv_heads < 1) return SKV_ERR_INVALID;
+  if (num_qo_heads % num_kv_heads != 0 || num_sms < 0) return SKV_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128) return SKV_ERR_UNSUPPORTED;
+  if (num_qo_heads > 65535) return SKV_ERR_UNSUPPORTED;
+  const int32_t* kv = kv_indptr_h != nullptr ? kv_indptr_h : qo_indptr_h;
+  if (qo_indptr_h[0] != 0 || kv[0] != 0) return SKV_ERR_INVALID;
+  for (int32_t r = 0; r < batch; ++r)
+    if (qo_indptr_h[r + 1] < qo_indptr_h[r] || kv[r + 1] < kv[r]) return SKV_ERR_INVALID;
+  const int32_t ctas = num_sms > 0 ? num_sms : device_sm_count();
+  const bool heads = (num_qo_heads / num_kv_heads) % 2 == 0;  // A and B: two heads, else two token tiles
+  const int32_t step = heads ? kPromptTile : 2 * kPromptTile;
+
+  // token tiles: first token, tokens, key tiles its last token needs
+  struct Span {
+    int32_t r, q0, n, tiles;
+  };
+  std::vector<Span> spans;
+  int64_t total = 0;
+  const int32_t head_items = heads ? num_qo_heads / 2 : num_qo_heads;
+  for (int32_t r = 0; r < batch; ++r) {
+    const int64_t n = (int64_t)qo_indptr_h[r + 1] - qo_indptr_h[r], len = (int64_t)kv[r + 1] - kv[r];
+    for (int64_t q0 = 0; q0 < n; q0 += step) {
+      const int64_t m = std::min<int64_t>(step, n - q0);
+      const int64_t seen = causal ? std::min(len, std::max<int64_t>(0, len - n + q0 + m)) : len;
+      const int64_t tiles = (seen + kPromptTile - 1) / kPromptTile;
+      spans.push_back(Span{r, (int32_t)q0, (int32_t)m, (int32_t)tiles});
+      total += std::max<int64_t>(tiles, 1) * head_items;
+    }
+  }
+  // a span longer than 1.5 shares of the whole work is cut along the keys (pieces of >= 8 tiles)
+  const int64_t chunk = std::max<int64_t>(8, (total + ctas - 1) / ctas);
+  std::vector<PromptItem> items;
+  std::vector<MergeItem> merges;
+  int64_t part_rows = 0;
+  for (const Span& s : spans) {
+    const int64_t n = (int64_t)qo_indptr_h[s.r + 1] - qo_indptr_h[s.r], len = (int64_t)kv[s.r + 1] - kv[s.r];
+    const int32_t pieces = 2 * (int64_t)s.tiles > 3 * chunk ? (int32_t)((s.tiles + chunk - 1) / chunk) : 1;
+    info->max_splits = std::max(info->max_splits, pieces);
+    info->total_splits += pieces;
+    if (part_rows + (int64_t)s.n * pieces > INT32_MAX) return SKV_ERR_UNSUPPORTED;
+    for (int32_t j = 0; j < pieces; ++j) {
+      PromptItem w;
+      std::memset(&w, 0, sizeof(w));
+      w.q0a = qo_indptr_h[s.r] + s.q0;
+      w.na = std::min(s.n, kPromptTile);
+      w.limit_a = (int32_t)(len - n + s.q0 + 1);
+      w.q0b = heads ? w.q0a : w.q0a + kPromptTile;
+      w.nb = heads ? w.na : s.n - w.na;
+      w.limit_b = heads ? w.limit_a : w.limit_a + kPromptTile;
+      w.kv0 = kv[s.r];
+      w.kv_len = (int32_t)len;
+      w.tile_begin = (int32_t)((int64_t)s.tiles * j / pieces);
+      w.tile_end = (int32_t)((int64_t)s.tiles * (j + 1) / pieces);
+      w.part_row = pieces > 1 ? (int32_t)(part_rows + j) : -1;
+      w.part_stride = pieces;
+      w.causal = causal != 0;
+      for (int32_t h = 0; h < num_qo_heads; h += heads ? 2 : 1) {
+        w.ha = h;
+        w.hb = heads ? h + 1 : h;
+        items.push_back(w);
+      }
+    }
+    if (pieces > 1) {
+      for (int32_t t = 0; t < s.n; ++t)
+        merges.push_back(MergeItem{qo_indptr_h[s.r] + s.q0 + t, (int32_t)(part_rows + (int64_t)t * pieces), pieces, 0});
+      part_rows += (int64_t)s.n * pieces;
+    }
+  }
+  // longest first onto the least loaded CTA; an item costs its tiles for both query tiles, and a
+  // start and end worth about one and a half tiles
+  const auto cost = [](const PromptItem& w) {
+    return (int64_t)(w.tile_end - w.tile_begin) * (w.nb > 0 ? 2 : 1) + 3;
+  };
+  std::vector<int32_t> order(items.size());
+  for (size_t i = 0; i < items.size(); ++i) order[i] = (int32_t)i;
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int32_t x, int32_t y) { return cost(items[x]) > cost(items[y]); });
+  const int32_t g = (int32_t)std::min<size_t>(items.size(), (size_t)ctas);
+  using Load = std::pair<int64_t, int32_t>;
+  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> least;
+  for (int32_t c = 0; c < g; ++c) least.push({0, c});
+  std::vector<int32_t> owner(items.size()), indptr(g + 1, 0);
+  for (int32_t i : order) {
+    Load l = least.top();
+    least.pop();
+    owner[i] = l.second;
+    ++indptr[l.second + 1];
+    l.first += cost(items[i]);
+    least.push(l);
+  }
+  for (int32_t c = 0; c < g; ++c) indptr[c + 1] += indptr[c];
+
+  const int64_t words = 16LL * (int64_t)items.size() + 4LL * (int64_t)merges.size() + (g > 0 ? g + 1 : 0);
+  if (words > INT32_MAX) return SKV_ERR_UNSUPPORTED;
+  info->num_work = (int32_t)items.size();
+  info->num_partial_rows = (int32_t)part_rows;
+  info->num_merge_rows = (int32_t)merges.size();
+  info->kernel = KERNEL_PROMPT;
+  info->q_tile = kPromptTile;
+  info->plan_words = (int32_t)words;
+  info->num_ctas = g;
+  info->cta_offset = (int32_t)(16LL * (int64_t)items.size() + 4LL * (int64_t)merges.size());
+  if (plan_h == nullptr || plan_capacity < words) return words == 0 ? SKV_OK : SKV_ERR_WORKSPACE;
+  std::vector<int32_t> at(indptr.begin(), indptr.end() - 1);
+  PromptItem* out = reinterpret_cast<PromptItem*>(plan_h);
+  for (int32_t i : order) out[at[owner[i]]++] = items[i];
+  if (!merges.empty()) std::memcpy(plan_h + 16 * items.size(), merges.data(), merges.size() * sizeof(MergeItem));
+  if (g > 0) std::memcpy(plan_h + info->cta_offset, indptr.data(), (g + 1) * sizeof(int32_t));
+  return SKV_OK;
+} catch (...) {
+  return SKV_ERR_INVALID;  // out of host memory
+}
+
+skv_status skv_prompt_attn_fwd(const skv_prompt_params* p, const int32_t* plan_d, const skv_plan_info* info,
+                               skv_stream_t stream) {
+  if (p == nullptr || info == nullptr || info->kernel != KERNEL_PROMPT) return SKV_ERR_INVALID;
+  if (info->num_work < 0 || info->num_merge_rows < 0 || info->num_partial_rows < 0) return SKV_ERR_INVALID;
+  if (p->total_q < 0 || p->total_kv < 0 || p->num_qo_heads < 1 || p->num_kv_heads < 1) return SKV_ERR_INVALID;
+  if (p->num_qo_heads % p->num_kv_heads != 0) return SKV_ERR_INVALID;
+  if (p->head_dim != 64 && p->head_dim != 128) return SKV_ERR_UNSUPPORTED;
+  if (p->num_qo_heads > 65535) return SKV_ERR_UNSUPPORTED;
+  if (p->o_dtype != SKV_F32 && p->o_dtype != SKV_BF16) return SKV_ERR_UNSUPPORTED;
+  if (!(p->sm_scale > 0.f) || !std::isfinite(p->sm_scale)) return SKV_ERR_INVALID;
+  if (info->num_work == 0 || p->total_q == 0) return SKV_OK;  // no query rows: nothing to launch
+  if (plan_d == nullptr || info->num_ctas < 1 ||
+      info->cta_offset < 16LL * info->num_work + 4LL * info->num_merge_rows)
+    return SKV_ERR_INVALID;
+  if (!p->o || (p->total_kv > 0 && (!p->k || !p->v))) return SKV_ERR_INVALID;
+  const int32_t rows[3] = {p->total_q, p->total_kv, p->total_kv};
+  const int32_t head_count[3] = {p->num_qo_heads, p->num_kv_heads, p->num_kv_heads};
+  const void* base[3] = {p->q, p->k, p->v};
+  const int64_t* stride[3] = {p->q_stride, p->k_stride, p->v_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (rows[i] == 0) continue;
+    if (base[i] == nullptr) return SKV_ERR_INVALID;
+    if (!aligned16(base[i])) return SKV_ERR_ALIGNMENT;
+    const int32_t count[2] = {rows[i], head_count[i]};
+    for (int d = 0; d < 2; ++d) {
+      if (count[d] <= 1) continue;  // never used
+      if (stride[i][d] <= 0) return SKV_ERR_INVALID;
+      if (stride[i][d] % 8 != 0) return SKV_ERR_ALIGNMENT;
+      if (stride[i][d] >= (1LL << 38)) return SKV_ERR_UNSUPPORTED;  // 2^40 bytes: the tensor map's limit
+    }
+  }
+  if (!aligned16(p->o) || !aligned16(p->o_part)) return SKV_ERR_ALIGNMENT;
+  if (info->num_partial_rows > 0 && (!p->o_part || !p->lse_part)) return SKV_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int e = launch_prompt_attn(*p, reinterpret_cast<const PromptItem*>(plan_d), plan_d + info->cta_offset,
+                                   info->num_ctas, s);
+  if (e != 0 || info->num_merge_rows == 0) return cuda_status(e);
+  const MergeItem* merges = reinterpret_cast<const MergeItem*>(plan_d + 16LL * info->num_work);
+  return cuda_status(launch_merge(p->o_part, p->lse_part, nullptr, 0, merges, info->num_merge_rows, p->num_qo_heads,
+                                  p->head_dim, p->o, p->o_dtype, p->lse, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,537 @@
+// Attention over whole prompts: packed sequences of different lengths, grouped heads, causal or not,
+// keys and values as the projections left them ([token, head, dim], any 16-byte strides).
+//   s = sm_scale q . k,  O = softmax(s) v,  LSE = ln sum e^s;  with the causal mask the n query tokens
+//   of a sequence of L keys are its last n positions, query token i sees keys t <= L - n + i.
+//
+// Bound by the tensor cores and the exponentials together: a 128 x 128 score tile costs two
+// 128 x 128 x D products (1024 cycles at D = 128) and 16384 exponentials (1024 cycles at 16 per SM).
+// Hence two query tiles per CTA, A and B, that take turns: while the softmax warps of A work on
+// S_A, the tensor cores run P_B V and Q_B K^T.  A and B are two heads of one group on the same
+// tokens (they share every K and V tile), or, for odd groups, consecutive 128-token tiles of a head.
+//
+// TMEM holds S_A, S_B (128 fp32 columns each) and O_A, O_B; P (bf16) overwrites the first half of its
+// own S and is the A operand of P V straight from TMEM.  MMAs of one CTA are issued by one thread
+// and complete in order, so two facts need no barrier of their own: Q K^T of the next tile may
+// overwrite S / P as soon as it is issued after P V, and a full S means the P V before it is done,
+// so the softmax warps may rescale O.  The running maximum is raised only when a score passes it
+// by 2^8, so after the first tiles O is rarely rescaled.
+//
+// Persistent: the planner hands every CTA a list of items (a pair of query tiles and a range of
+// key tiles), longest first onto the least loaded.  Items of few rows over many keys are cut along
+// the keys into fp32 partials that the merge pass joins.  Roles: warps 0-3 softmax of A, 4-7 of B,
+// warp 8 TMA (ring of K and V tiles in the order of use), warp 9 MMA.  All waits are bounded.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "prompt_plan.h"
+#include "tc_ptx.cuh"
+
+namespace skv {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 384;         // three warpgroups; the last one's warps 2 and 3 idle
+// Registers: 384 threads start with 168; the softmax warpgroups hold a whole row of scores, so they
+// take 208 and the third gives up to 88 (2 x 128 x 208 + 128 x 88 = 384 x 168).
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "the split fits the launch's registers");
+constexpr int kRegion = kTile * 128;  // 16 KB: 128 rows of 64 bf16
+constexpr float kRaise = 8.f;
+
+template <int D>
+struct Smem {
+  static constexpr int tile = D / 64 * kRegion;
+  static constexpr int slots = D == 128 ? 5 : 8;
+  static constexpr int q = 0;                       // Q_A, Q_B
+  static constexpr int kv = 2 * tile;
+  static constexpr int bars = kv + slots * tile;
+  static constexpr int nbars = 2 * slots + 2 + 6;
+  static constexpr int misc = bars + nbars * 8;
+  static constexpr int total = misc + 16;
+};
+static_assert(Smem<128>::total + 1024 <= 232448, "fits the 227 KB opt-in shared memory");
+
+struct PromptArgs {
+  const PromptItem* items;
+  const int32_t* cta_indptr;
+  int hq, group, total_q;
+  float scale_log2;
+  void* o;
+  float* lse;
+  float* o_part;
+  float* lse_part;
+  int32_t* status;
+};
+
+// D[tmem] (+)= A[tmem] . B[smem], kind::f16: A rows in TMEM lanes, two bf16 per column
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void upk2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The two query tiles of an item, and the key tiles [0, tiles) of its range that each one needs.
+struct Side {
+  int q0, n, head, limit, tiles;
+};
+__device__ __forceinline__ Side side_of(const PromptItem& w, int x) {
+  Side s;
+  s.q0 = x ? w.q0b : w.q0a;
+  s.n = x ? w.nb : w.na;
+  s.head = x ? w.hb : w.ha;
+  s.limit = x ? w.limit_b : w.limit_a;  // keys the tile's first token sees (all of them: not causal)
+  const int64_t most = w.causal ? min((int64_t)w.kv_len, (int64_t)s.limit + s.n - 1) : (int64_t)w.kv_len;
+  const int end = most > 0 ? (int)((most + kTile - 1) / kTile) : 0;
+  s.tiles = s.n > 0 ? max(0, min(w.tile_end, end) - w.tile_begin) : 0;
+  return s;
+}
+
+template <int D, typename OutT>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const PromptArgs a) {
+  using S = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = tc::smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  tc::grid_launch_dependents();  // the merge pass may be scheduled; it waits for this grid
+
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::misc + 4);
+  const uint32_t bar0 = sbase + S::bars;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S::slots + s); };
+  const uint32_t qfull = bar0 + 8u * (2 * S::slots), qempty = qfull + 8;
+  auto sfull_bar = [&](int x) { return qempty + 8u + 8u * x; };
+  auto pfull_bar = [&](int x) { return qempty + 24u + 8u * x; };
+  auto ofull_bar = [&](int x) { return qempty + 40u + 8u * x; };
+
+  if (tid == 0) {
+    for (int s = 0; s < S::slots; ++s) {
+      tc::mbar_init(full_bar(s), 1);
+      tc::mbar_init(empty_bar(s), 1);
+    }
+    tc::mbar_init(qfull, 1);
+    tc::mbar_init(qempty, 1);
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(sfull_bar(x), 1);
+      tc::mbar_init(pfull_bar(x), 4);
+      tc::mbar_init(ofull_bar(x), 1);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 9) tc::tmem_alloc(tc::smem_u32(tmem_holder), 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tm_s[2] = {tmem, tmem + kTile}, tm_o[2] = {tmem + 2 * kTile, tmem + 3 * kTile};
+  const int i_begin = a.cta_indptr[blockIdx.x], i_end = a.cta_indptr[blockIdx.x + 1];
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+      // ==================================================================================== TMA
+      int slot_it = 0, q_it = 0;  // ring loads and Q loads so far
+      bool ok = true;
+      auto load_kv = [&](const CUtensorMap* map, int head, int row) {
+        const int st = slot_it % S::slots;
+        if (slot_it >= S::slots) ok = tc::mbar_wait(empty_bar(st), ((slot_it / S::slots) + 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(full_bar(st), (uint32_t)S::tile);
+          for (int r = 0; r < D / 64; ++r)
+            tc::tma_load_3d(sbase + S::kv + st * S::tile + r * kRegion, map, full_bar(st), r * 64, head, row);
+        }
+        ++slot_it;
+      };
+      if (lane == 0) {
+        tc::prefetch_tmap(&qmap);
+        tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&vmap);
+      }
+      for (int i = i_begin; i < i_end && ok; ++i) {
+        const PromptItem w = a.items[i];
+        const Side sa = side_of(w, 0), sb = side_of(w, 1);
+        const int tiles = max(sa.tiles, sb.tiles);
+        if (tiles == 0) continue;
+        if (q_it > 0) ok = tc::mbar_wait(qempty, (q_it + 1) & 1, abort_flag, a.status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          const int sides = (sa.tiles > 0) + (sb.tiles > 0);
+          tc::mbar_arrive_expect_tx(qfull, (uint32_t)(sides * S::tile));
+          for (int r = 0; r < D / 64; ++r) {
+            if (sa.tiles > 0) tc::tma_load_3d(sbase + S::q + r * kRegion, &qmap, qfull, r * 64, sa.head, sa.q0);
+            if (sb.tiles > 0) tc::tma_load_3d(sbase + S::q + S::tile + r * kRegion, &qmap, qfull, r * 64, sb.head, sb.q0);
+          }
+        }
+        ++q_it;
+        const int kh = w.ha / a.group, row0 = w.kv0 + w.tile_begin * kTile;
+        load_kv(&kmap, kh, row0);
+        for (int j = 0; j < tiles && ok; ++j) {  // in the order of use: K(j + 1), V(j)
+          if (j + 1 < tiles) load_kv(&kmap, kh, row0 + (j + 1) * kTile);
+          if (ok) load_kv(&vmap, kh, row0 + j * kTile);
+        }
+      }
+      if (!ok && lane == 0) {  // copies in flight may still be landing: wait for them (bounded)
+        auto drain = [&](uint32_t bar, uint32_t parity) {
+          const uint64_t t0 = tc::globaltimer_ns();
+          while (!tc::mbar_try_wait(bar, parity) && tc::globaltimer_ns() - t0 < 20000000ull) {
+          }
+        };
+        for (int t = max(0, slot_it - S::slots); t < slot_it; ++t) drain(full_bar(t % S::slots), (t / S::slots) & 1);
+        if (q_it > 0) drain(qfull, (q_it - 1) & 1);
+      }
+    } else if (warp == 9) {
+      // ==================================================================================== MMA
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, kTile, false, false);
+        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, false, true);
+        int slot_it = 0, q_it = 0, p_it[2] = {0, 0};
+        bool ok = true;
+        auto wait_slot = [&]() {
+          const int st = slot_it % S::slots;
+          ok = tc::mbar_wait(full_bar(st), (slot_it / S::slots) & 1, abort_flag, a.status);
+          tc::tc_fence_after();
+          ++slot_it;
+          return st;
+        };
+        auto qk = [&](int x, int st) {
+          const uint32_t qs = sbase + S::q + x * S::tile, ks = sbase + S::kv + st * S::tile;
+  #pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_bf16(tm_s[x], tc::sdesc_sw128(qs + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024),
+                         tc::sdesc_sw128(ks + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
+          tc::mma_commit(sfull_bar(x));
+        };
+        for (int i = i_begin; i < i_end && ok; ++i) {
+          const PromptItem w = a.items[i];
+          const Side s[2] = {side_of(w, 0), side_of(w, 1)};
+          const int tiles = max(s[0].tiles, s[1].tiles);
+          if (tiles == 0) continue;
+          ok = tc::mbar_wait(qfull, q_it & 1, abort_flag, a.status);
+          ++q_it;
+          if (!ok) break;
+          int kst = wait_slot();
+          if (!ok) break;
+  #pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (s[x].tiles > 0) qk(x, kst);
+          tc::mma_commit(empty_bar(kst));
+          if (tiles == 1) tc::mma_commit(qempty);
+          for (int j = 0; j < tiles && ok; ++j) {
+            const bool more = j + 1 < tiles;
+            if (more) kst = wait_slot();
+            if (!ok) break;
+            const int vst = wait_slot();
+            if (!ok) break;
+            const uint32_t vs = sbase + S::kv + vst * S::tile;
+  #pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (j < s[x].tiles) {
+                ok = tc::mbar_wait(pfull_bar(x), p_it[x] & 1, abort_flag, a.status);
+                ++p_it[x];
+                if (!ok) break;
+                tc::tc_fence_after();
+  #pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 packed columns of P
+                  mma_ts(tm_o[x], tm_s[x] + k * 8, tc::sdesc_sw128(vs + k * 2048, kRegion, 1024), idesc_o,
+                         (j > 0 || k > 0) ? 1u : 0u);
+                if (j + 1 == s[x].tiles) tc::mma_commit(ofull_bar(x));
+              }
+              if (j + 1 < s[x].tiles) qk(x, kst);
+            }
+            if (!ok) break;
+            if (more) tc::mma_commit(empty_bar(kst));
+            if (j + 2 == tiles) tc::mma_commit(qempty);
+            tc::mma_commit(empty_bar(vst));
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ================================================================================ softmax
+    const int x = warp >> 2, quarter = warp & 3;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tm_s[x] + lane_base, to = tm_o[x] + lane_base;
+    const int r = quarter * 32 + lane;  // this thread's row of the tile
+    int s_it = 0, o_it = 0;
+    int v_seq = 0;  // ring loads of the items before this one
+    bool ok = true;
+    for (int i = i_begin; i < i_end; ++i) {
+      const PromptItem w = a.items[i];
+      const Side s_me = side_of(w, x), s_other = side_of(w, 1 - x);
+      const int tiles = s_me.tiles, all_tiles = max(tiles, s_other.tiles);
+      // l: sum of the exact weights (for the LSE); lr: of the rounded ones that P V multiplies (the
+      // divisor of O, so that a row with one dominant key returns that key's V)
+      float m = -INFINITY, l = 0.f, lr = 0.f;
+      const int64_t lim64 = w.causal ? min((int64_t)w.kv_len, (int64_t)s_me.limit + r) : (int64_t)w.kv_len;
+      const int limit = (int)max(lim64, (int64_t)0);
+      const int warp_limit = __shfl_sync(0xffffffffu, limit, 0);  // the warp's first row sees fewest
+      for (int j = 0; j < tiles; ++j) {
+        const int key0 = (w.tile_begin + j) * kTile;
+        ok = tc::mbar_wait(sfull_bar(x), s_it & 1, abort_flag, a.status) && ok;
+        ++s_it;
+        tc::tc_fence_after();
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 16) {
+          float v[16];
+          tc::tmem_ld_x16(ts + c, v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[c + e] = v[e];
+        }
+        tc::tmem_wait_ld();
+        if (key0 + kTile > warp_limit) {
+          const int nv = limit - key0;
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) s[c] = c < nv ? s[c] : -INFINITY;
+        }
+        float mx;
+        {
+          float q[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            q[u] = max3(s[32 * u], s[32 * u + 1], s[32 * u + 2]);
+#pragma unroll
+            for (int e = 3; e < 31; e += 2) q[u] = max3(q[u], s[32 * u + e], s[32 * u + e + 1]);
+            q[u] = fmaxf(q[u], s[32 * u + 31]);
+          }
+          mx = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])) * a.scale_log2;  // the scale is positive
+        }
+        const bool raise = mx > m + kRaise;
+        if (__any_sync(0xffffffffu, raise)) {  // warp-uniform: TMEM access is warp-collective
+          const float mn = raise ? mx : m;
+          const float al = mn == m ? 1.f : ex2(m - mn);
+          l *= al;
+          lr *= al;
+          m = mn;
+          if (j > 0) {  // a full S(j) means P V(j - 1) is done
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              float v[16];
+              tc::tmem_ld_x16(to + c, v);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] *= al;
+              tc::tmem_st_x16(to + c, v);
+            }
+          }
+        }
+        if (key0 + kTile > w.kv_len && (x == 0 || j >= s_other.tiles)) {
+          // keys past the sequence belong to another one (or to nobody): their V rows become zero,
+          // by A's warps, or by B's where A has no such tile
+          const int seq = v_seq + (j + 1 < all_tiles ? 2 * j + 2 : 2 * j + 1);  // ring position of V(j)
+          const int st = seq % S::slots;
+          ok = tc::mbar_wait(full_bar(st), (seq / S::slots) & 1, abort_flag, a.status) && ok;
+          uint8_t* vb = smem + S::kv + st * S::tile;
+          if (r >= w.kv_len - key0) {
+#pragma unroll
+            for (int rgn = 0; rgn < D / 64; ++rgn)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<uint4*>(vb + rgn * kRegion + r * 128)[e] = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        const float mm = m == -INFINITY ? 0.f : m;
+        const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-mm, -mm);
+        uint64_t la[2] = {0, 0}, lb[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float pw[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            upk2(fma2(pk2(s[c + e], s[c + e + 1]), sc2, nm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h2);
+            pw[e >> 1] = __uint_as_float(u);
+            la[(e >> 1) & 1] = add2(la[(e >> 1) & 1], pk2(p0, p1));
+            lb[(e >> 1) & 1] = add2(lb[(e >> 1) & 1], pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)));
+          }
+          tc::tmem_st_x16(ts + c / 2, pw);
+        }
+        {
+          float a0, a1, b0, b1;
+          upk2(add2(la[0], la[1]), a0, a1);
+          upk2(add2(lb[0], lb[1]), b0, b1);
+          l += a0 + a1;
+          lr += b0 + b1;
+        }
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(pfull_bar(x));
+      }
+      v_seq += 2 * all_tiles;
+      if (tiles > 0) {
+        ok = tc::mbar_wait(ofull_bar(x), o_it & 1, abort_flag, a.status) && ok;
+        ++o_it;
+        tc::tc_fence_after();
+      }
+      const bool live = r < s_me.n && s_me.q0 + r < a.total_q;
+      const bool some = l > 0.f || l != l;
+      const float inv = some ? 1.f / lr : 0.f;
+      OutT* oo = nullptr;
+      float* op = nullptr;
+      if (live) {
+        const float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+        const int64_t row = s_me.q0 + r;
+        if (w.part_row < 0) {
+          oo = reinterpret_cast<OutT*>(a.o) + (row * a.hq + s_me.head) * D;
+          if (a.lse != nullptr) a.lse[row * a.hq + s_me.head] = lse;
+        } else {
+          const int64_t part = (int64_t)w.part_row + (int64_t)(row - w.q0a) * w.part_stride;
+          op = a.o_part + (part * a.hq + s_me.head) * D;
+          a.lse_part[part * a.hq + s_me.head] = lse;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        if (tiles > 0) {  // the whole warp loads; live rows store
+          tc::tmem_ld_x16(to + c, v);
+          tc::tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = some ? v[e] * inv : 0.f;
+        if (op != nullptr || (oo != nullptr && sizeof(OutT) == 4)) {
+          float* dst = (op != nullptr ? op : reinterpret_cast<float*>(oo)) + c;
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        } else if (oo != nullptr) {
+          uint32_t u[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(oo + c);
+          dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+          dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        }
+      }
+      tc::tc_fence_before();  // O has been read before the next item's first P is announced
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// [rows, heads, D] bf16 with (row, head) strides in elements; 128-row boxes of one head's 64 columns.
+bool rows_map(CUtensorMap* m, const void* base, int rows, int heads, int head_dim, const int64_t* stride) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  // the stride of a dimension of one entry is never used, but has to be a valid one
+  const cuuint64_t head_st = heads > 1 ? (cuuint64_t)stride[1] * 2 : (cuuint64_t)head_dim * 2;
+  const cuuint64_t row_st = rows > 1 ? (cuuint64_t)stride[0] * 2 : (cuuint64_t)head_dim * 2 * heads;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t st[2] = {head_st, row_st};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, st, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, typename OutT>
+int launch_t(const CUtensorMap* maps, const PromptArgs& a, int ctas, cudaStream_t s) {
+  static DeviceSmemAttr attr;
+  const int smem = Smem<D>::total + 1024;
+  if (const int e = attr.ensure(reinterpret_cast<const void*>(prompt_attn_kernel<D, OutT>), smem)) return e;
+  prompt_attn_kernel<D, OutT><<<ctas, kThreads, smem, s>>>(maps[0], maps[1], maps[2], a);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_prompt_attn(const skv_prompt_params& p, const PromptItem* items, const int32_t* cta_indptr, int num_ctas,
+                       cudaStream_t s) {
+  CUtensorMap maps[3];
+  if (!rows_map(&maps[0], p.q, p.total_q, p.num_qo_heads, p.head_dim, p.q_stride)) return (int)cudaErrorInvalidValue;
+  if (p.total_kv > 0) {
+    if (!rows_map(&maps[1], p.k, p.total_kv, p.num_kv_heads, p.head_dim, p.k_stride) ||
+        !rows_map(&maps[2], p.v, p.total_kv, p.num_kv_heads, p.head_dim, p.v_stride))
+      return (int)cudaErrorInvalidValue;
+  } else {  // no key anywhere: the maps are never used
+    maps[1] = maps[0];
+    maps[2] = maps[0];
+  }
+  PromptArgs a;
+  a.items = items;
+  a.cta_indptr = cta_indptr;
+  a.hq = p.num_qo_heads;
+  a.group = p.num_qo_heads / p.num_kv_heads;
+  a.total_q = p.total_q;
+  a.scale_log2 = p.sm_scale * kLog2e;
+  a.o = p.o;
+  a.lse = p.lse;
+  a.o_part = p.o_part;
+  a.lse_part = p.lse_part;
+  a.status = p.status;
+  const bool bf16 = p.o_dtype == SKV_BF16;
+  if (p.head_dim == 128)
+    return bf16 ? launch_t<128, __nv_bfloat16>(maps, a, num_ctas, s) : launch_t<128, float>(maps, a, num_ctas, s);
+  return bf16 ? launch_t<64, __nv_bfloat16>(maps, a, num_ctas, s) : launch_t<64, float>(maps, a, num_ctas, s);
+}
+
+}  // namespace skv

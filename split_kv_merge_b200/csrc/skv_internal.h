@@ -31,6 +31,7 @@ enum KernelId : int32_t {
   KERNEL_GQA_TC_WIDE = 3,
   KERNEL_GQA_TC_PREFILL = 4,  // tensor-core, 128 query rows (tokens x group heads) per unit
   KERNEL_GQA_SCALED = 5,      // 8-bit cache with block scales, 8 or 16 query rows per tile
+  KERNEL_PROMPT = 6,          // packed prompts, two 128-row query tiles per item
   KERNEL_MLA_SIMT = 11,
   KERNEL_MLA_TC16 = 12,  // tensor-core MLA, 16 query rows per unit (bf16 or e4m3 cache)
   KERNEL_MLA_TC32 = 13,  // tensor-core MLA, 32 query rows per unit (bf16 or e4m3 cache)

@@ -8,9 +8,9 @@ from typing import Optional
 
 import numpy as np
 
-from . import (AppendParams, BF16, E4M3, F32, I8, PagedParams, PagedScaledParams, Plan, Rope, RopeParams, _check,
-               _index_ptr, _kv_append, _ROPE, _ROPE_SCALING, _rope_apply, _rope_frequencies, _scaled_fwd,
-               plan_paged_scaled)
+from . import (AppendParams, BF16, E4M3, F32, I8, PagedParams, PagedScaledParams, Plan, PromptParams, Rope,
+               RopeParams, _check, _index_ptr, _kv_append, _prompt_fwd, _ROPE, _ROPE_SCALING, _rope_apply,
+               _rope_frequencies, _scaled_fwd, plan_paged_scaled, plan_prompt)
 
 _NULL = nullcontext()
 
@@ -275,4 +275,51 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
         p = PagedScaledParams(base, k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(), v_scale.stride(), block)
         _check(_scaled_fwd(ctypes.byref(p), plan.device.data_ptr(), ctypes.byref(plan.info), _stream(stream, dev)),
                "skv_paged_attn_scaled_fwd")
+    return o, lse, {"plan": plan, "o_part": o_part, "lse_part": lse_part}
+
+
+def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = True, sm_scale: Optional[float] = None,
+                     o_dtype=None, plan: Optional[Plan] = None, status=None, stream=None, o_out=None, lse_out=None):
+    """Attention over packed prompts (skv_prompt_attn_fwd): q [total_q, Hq, D], k, v [total_kv, Hk, D] bf16, any
+    token / head strides; sequence r has query rows qo_indptr_h[r] .. and key rows kv_indptr_h[r] ..
+    (default: the same rows).  ``causal``: its query tokens are its last positions.  ``plan``
+    (``plan_prompt`` with the same ``causal``) may be kept over the layers of a step.  Rows of outputs given as
+    ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
+    Returns (o, lse, extras) with extras = {"plan", "o_part", "lse_part"}."""
+    import torch
+    _need(q.dim() == 3 and k.dim() == 3, "q is [total_q, Hq, D], k and v are [total_kv, Hk, D]")
+    dev, total_q, hq, dim = q.device, q.shape[0], q.shape[1], q.shape[2]
+    total_kv, hk = k.shape[0], k.shape[1]
+    _need(q.dtype == torch.bfloat16 and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16,
+          "q, k and v must be bfloat16")
+    _rows3("q", q, total_q, dim)
+    _rows3("k", k, total_kv, dim)
+    _rows3("v", v, total_kv, dim)
+    _need(v.shape[1] == hk, "k and v must have the same heads")
+    _on(dev, k=k, v=v, status=status, o_out=o_out, lse_out=lse_out)
+    _need(len(qo_indptr_h) > 0 and total_q >= int(qo_indptr_h[-1]), "q has fewer rows than qo_indptr names")
+    _need(total_kv >= int((qo_indptr_h if kv_indptr_h is None else kv_indptr_h)[-1]),
+          "k and v have fewer rows than kv_indptr names")
+    for name, t, shape in (("o_out", o_out, (total_q, hq, dim)), ("lse_out", lse_out, (total_q, hq))):
+        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous()), f"{name} must be contiguous {shape}")
+    _need(lse_out is None or lse_out.dtype == torch.float32, "lse_out must be float32")
+    out_dtype = o_out.dtype if o_out is not None else (o_dtype or torch.float32)
+    _need(out_dtype in (torch.float32, torch.bfloat16), "outputs are float32 or bfloat16")
+    with _device(dev), _on_stream(stream, dev):
+        if plan is None:
+            plan = plan_prompt(qo_indptr_h, kv_indptr_h, hq, hk, dim, causal)
+        if plan.device is None:
+            plan.to(dev)
+        o = torch.empty(total_q, hq, dim, dtype=out_dtype, device=dev) if o_out is None else o_out
+        lse = torch.empty(total_q, hq, dtype=torch.float32, device=dev) if lse_out is None else lse_out
+        n_part = plan.info.num_partial_rows
+        o_part = torch.empty(n_part, hq, dim, dtype=torch.float32, device=dev) if n_part else None
+        lse_part = torch.empty(n_part, hq, dtype=torch.float32, device=dev) if n_part else None
+        p = PromptParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride()[:2], k.stride()[:2], v.stride()[:2], total_q,
+                         total_kv, hq, hk, dim, dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(),
+                         BF16 if out_dtype == torch.bfloat16 else F32, lse.data_ptr(),
+                         o_part.data_ptr() if n_part else None, lse_part.data_ptr() if n_part else None,
+                         None if status is None else status.data_ptr())
+        _check(_prompt_fwd(ctypes.byref(p), plan.device.data_ptr(), ctypes.byref(plan.info), _stream(stream, dev)),
+               "skv_prompt_attn_fwd")
     return o, lse, {"plan": plan, "o_part": o_part, "lse_part": lse_part}

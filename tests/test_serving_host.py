@@ -259,3 +259,115 @@ def test_scaled_struct_layout():
         pytest.skip("needs a C compiler")
     got, want = c_layout([(skv.PagedScaledParams, "skv_paged_scaled_params")])
     assert got == want
+
+
+def _plan_prompt(qo, kv, hq=4, hk=2, d=64, causal=1, sms=148, batch=None):
+    q = None if qo is None else np.asarray(qo, np.int32)
+    k = None if kv is None else np.asarray(kv, np.int32)
+    info, plan = skv.PlanInfo(), np.zeros(1 << 20, np.int32)
+    code = skv._plan_prompt(len(qo) - 1 if batch is None else batch, skv._ptr_i32(q), skv._ptr_i32(k), hq, hk, d, causal,
+                            sms, skv._ptr_i32(plan), plan.size, ctypes.byref(info))
+    return code, plan, info
+
+
+@pytest.mark.parametrize("args,kw,code", [
+    (([0, 5], None), {}, skv.OK), (([0], None), {}, skv.OK), (([0, 0, 0], [0, 4, 4]), {}, skv.OK),
+    (([0, 5], None), dict(batch=-1), skv.ERR_INVALID), ((None, None), dict(batch=1), skv.ERR_INVALID),
+    (([1, 5], None), {}, skv.ERR_INVALID), (([0, 5, 3], None), {}, skv.ERR_INVALID),
+    (([0, 5], [0, -1]), {}, skv.ERR_INVALID), (([0, 5], [2, 5]), {}, skv.ERR_INVALID),
+    (([0, 5], None), dict(hq=5), skv.ERR_INVALID), (([0, 5], None), dict(hk=0), skv.ERR_INVALID),
+    (([0, 5], None), dict(d=80), skv.ERR_UNSUPPORTED), (([0, 5], None), dict(sms=-1), skv.ERR_INVALID),
+    (([0, 5], None), dict(hq=131072, hk=2), skv.ERR_UNSUPPORTED),
+])
+def test_plan_prompt_refusals(args, kw, code):
+    assert _plan_prompt(*args, **kw)[0] == code
+
+
+@pytest.mark.parametrize("hq,hk", [(4, 2), (3, 1), (5, 5), (8, 1)])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 300, 0, 128, 129], None), ([5, 64, 700], [4000, 20, 900]),
+                                            ([100], [30000]), ([7, 3], [0, 2])])
+def test_plan_prompt_covers_every_pair_once(hq, hk, causal, q_lens, kv_lens):
+    """Each (query token, head) meets each key tile that it sees in exactly one item; its partial rows and merge
+    items agree; the CTAs' lists hold every item once."""
+    kv_lens = q_lens if kv_lens is None else kv_lens
+    qo, kv = (np.concatenate([[0], np.cumsum(x)]) for x in (q_lens, kv_lens))
+    code, plan, info = _plan_prompt(qo, kv, hq, hk, 64, causal)
+    assert code == skv.OK and info.kernel == 6
+    items = plan[:16 * info.num_work].reshape(-1, 16)
+    merges = plan[16 * info.num_work:16 * info.num_work + 4 * info.num_merge_rows].reshape(-1, 4)
+    lists = plan[info.cta_offset:info.cta_offset + info.num_ctas + 1]
+    assert lists[0] == 0 and lists[-1] == info.num_work and np.all(np.diff(lists) >= 1) and info.num_ctas <= 148
+    merged = {int(m[0]): (int(m[1]), int(m[2])) for m in merges}
+    tiles = -(-max(max(kv_lens), 1) // 128)
+    met = np.zeros((int(qo[-1]), hq, tiles), int)
+    written = np.zeros((max(1, info.num_partial_rows), hq), int)
+    direct = np.zeros((int(qo[-1]), hq), int)
+    for w in items:
+        q0a, q0b, na, nb, ha, hb, la, lb, kv0, kv_len, t0, t1, part, stride, is_causal, _ = (int(v) for v in w)
+        r = int(np.searchsorted(qo, q0a, side="right")) - 1
+        assert (kv0, kv_len, is_causal) == (kv[r], kv_lens[r], causal) and ha // (hq // hk) == hb // (hq // hk)
+        for q0, n, h, lim in ((q0a, na, ha, la), (q0b, nb, hb, lb)):
+            assert 0 <= n <= 128 and q0 + n <= qo[r + 1] or n == 0
+            for i in range(n):
+                tok = q0 + i
+                assert lim + i == kv_lens[r] - q_lens[r] + (tok - qo[r]) + 1
+                met[tok, h, t0:t1] += 1
+                if part < 0:
+                    direct[tok, h] += 1
+                else:
+                    row = part + (tok - q0a) * stride
+                    written[row, h] += 1
+                    first, count = merged[tok]
+                    assert first <= row < first + count and count == stride
+    for tok in range(int(qo[-1])):
+        r = int(np.searchsorted(qo, tok, side="right")) - 1
+        sees = min(kv_lens[r], kv_lens[r] - q_lens[r] + tok - qo[r] + 1) if causal else kv_lens[r]
+        need = -(-max(0, sees) // 128)
+        assert np.all(met[tok, :, :need] == 1) and met[tok].max(initial=0) <= 1
+        assert np.all(direct[tok] == (0 if tok in merged else 1))
+    if info.num_partial_rows:
+        assert np.all(written == 1)
+        assert sum(c for _, c in merged.values()) == info.num_partial_rows
+
+
+def _prompt_params(**kw):
+    p = dict(q=PTR, k=PTR, v=PTR, q_stride=(256, 64), k_stride=(128, 64), v_stride=(128, 64), total_q=300, total_kv=9000,
+             num_qo_heads=4, num_kv_heads=2, head_dim=64, sm_scale=0.1, o=PTR, o_dtype=skv.F32, lse=PTR, o_part=PTR,
+             lse_part=PTR, status=None)
+    p.update(kw)
+    return skv.PromptParams(**p)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(total_q=-1), skv.ERR_INVALID), (dict(num_qo_heads=5), skv.ERR_INVALID), (dict(num_kv_heads=0), skv.ERR_INVALID),
+    (dict(head_dim=32), skv.ERR_UNSUPPORTED), (dict(o_dtype=skv.I8), skv.ERR_UNSUPPORTED),
+    (dict(sm_scale=0.0), skv.ERR_INVALID), (dict(sm_scale=-1.0), skv.ERR_INVALID), (dict(sm_scale=math.inf), skv.ERR_INVALID),
+    (dict(q=None), skv.ERR_INVALID), (dict(v=None), skv.ERR_INVALID), (dict(o=None), skv.ERR_INVALID),
+    (dict(k=PTR + 2), skv.ERR_ALIGNMENT), (dict(q_stride=(260, 64)), skv.ERR_ALIGNMENT),
+    (dict(k_stride=(128, 0)), skv.ERR_INVALID), (dict(v_stride=(-128, 64)), skv.ERR_INVALID),
+    (dict(k_stride=(1 << 38, 64)), skv.ERR_UNSUPPORTED), (dict(o_part=None), skv.ERR_WORKSPACE), (dict(total_q=0), skv.OK),
+])
+def test_prompt_fwd_refusals(change, code):
+    _, _, info = _plan_prompt([0, 100], [0, 9000])
+    assert info.num_partial_rows > 0
+    assert skv._prompt_fwd(ctypes.byref(_prompt_params(**change)), PTR, ctypes.byref(info), None) == code
+
+
+def test_prompt_fwd_needs_its_own_plan():
+    _, _, info = _plan_scaled()
+    assert skv._prompt_fwd(ctypes.byref(_prompt_params()), PTR, ctypes.byref(info), None) == skv.ERR_INVALID
+    assert skv._prompt_fwd(ctypes.byref(_prompt_params()), PTR, None, None) == skv.ERR_INVALID
+    _, _, info = _plan_prompt([0, 5], None)
+    assert skv._prompt_fwd(ctypes.byref(_prompt_params()), None, ctypes.byref(info), None) == skv.ERR_INVALID
+    assert skv._scaled_fwd(ctypes.byref(_scaled_params()), PTR, ctypes.byref(info), None) == skv.ERR_INVALID
+    with pytest.raises(ValueError):
+        skv.plan_prompt([0, 5], [0, 5, 6], 4, 2, 64)
+
+
+def test_prompt_struct_layout():
+    import shutil
+    if shutil.which("gcc") is None:
+        pytest.skip("needs a C compiler")
+    got, want = c_layout([(skv.PromptParams, "skv_prompt_params")])
+    assert got == want

@@ -1,77 +1,147 @@
-"""Serving operators around the attention calls: rotary positions and the cache append.  Argument
-checks and marshalling; the work runs in the library's kernels."""
+"""Serving operators around the paged attention calls: rotary positions, the cache append, attention
+over a block-scaled 8-bit cache and over packed prompts.  Argument checks and marshalling; the work runs
+in the library's kernels.
+
+A call costs the host about as much as the smallest kernels run, so parameter blocks are packed with
+``struct`` (layouts taken from the ctypes structures) and tensor properties are read once."""
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
+import struct
 from typing import Optional
 
 import numpy as np
 
-from . import (AppendParams, BF16, E4M3, F32, I8, PagedParams, PagedScaledParams, Plan, PromptParams, Rope,
-               RopeParams, _check, _index_ptr, _kv_append, _prompt_fwd, _ROPE, _ROPE_SCALING, _rope_apply,
-               _rope_frequencies, _scaled_fwd, plan_paged_scaled, plan_prompt)
-
-_NULL = nullcontext()
+from . import (AppendParams, BF16, E4M3, F32, I8, PagedScaledParams, Plan, PromptParams, RopeParams, SkvError,
+               _check, _index_ptr, _lib, _ROPE, _ROPE_SCALING, _rope_frequencies, plan_paged_scaled, plan_prompt)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _packer(cls) -> struct.Struct:
+    """``struct`` layout of a ctypes structure, its fields (nested ones and arrays too) in order."""
+    fmt, at = ["="], 0
+    code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_double: "d", ctypes.c_void_p: "Q"}
+
+    def walk(c, base):
+        nonlocal at
+        for name, kind in c._fields_:
+            offset = base + getattr(c, name).offset
+            if isinstance(kind, type) and issubclass(kind, ctypes.Structure):
+                walk(kind, offset)
+                continue
+            n, item = (kind._length_, kind._type_) if isinstance(kind, type) and issubclass(kind, ctypes.Array) else (1, kind)
+            fmt.append(f"{offset - at}x{n}{code[item]}")
+            at = offset + n * ctypes.sizeof(item)
+
+    walk(cls, 0)
+    fmt.append(f"{ctypes.sizeof(cls) - at}x")
+    return struct.Struct("".join(fmt))
 
 
-def _on(dev, **tensors) -> None:
-    """Every given tensor lives on the CUDA device ``dev``."""
+_pack_rope, _pack_append = _packer(RopeParams).pack, _packer(AppendParams).pack
+_pack_scaled, _pack_prompt = _packer(PagedScaledParams).pack, _packer(PromptParams).pack
+
+
+def _entry(name: str, args: int):
+    """The C function taking ``args`` addresses (a second prototype beside the binding's own)."""
+    return ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * args)((name, _lib))
+
+
+_call_rope, _call_append = _entry("skv_rope_apply", 2), _entry("skv_paged_kv_append", 2)
+_call_scaled, _call_prompt = _entry("skv_paged_attn_scaled_fwd", 4), _entry("skv_prompt_attn_fwd", 4)
+
+torch = _bf16 = _f32 = _i32 = _cache_codes = _raw_stream = _cuda_device = None
+
+
+def _init() -> None:
+    """Imports torch on the first call (planning alone needs numpy only)."""
+    global torch, _bf16, _f32, _i32, _cache_codes, _raw_stream, _cuda_device
+    import torch as t
+    _bf16, _f32, _i32 = t.bfloat16, t.float32, t.int32
+    _cache_codes = {t.bfloat16: BF16, t.float8_e4m3fn: E4M3, t.uint8: E4M3, t.int8: I8}
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda i: t.cuda.current_stream(i).cuda_stream)
+    _cuda_device = getattr(t._C, "_cuda_getDevice", None) or t.cuda.current_device
+    torch = t
+
+
+def _bad(what: str):
+    raise ValueError(what)
+
+
+def _device_index(t) -> int:
+    i = t.get_device()
+    if i < 0:
+        _bad("tensors must be on a CUDA device")
+    return i
+
+
+def _same_device(dev: int, **tensors) -> None:
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t is not None and t.get_device() != dev:
+            _bad(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _cache_code(dtype):
-    import torch
-    return {torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3, torch.uint8: E4M3, torch.int8: I8}.get(dtype)
+def _index(name: str, t, n: int, dev: int) -> int:
+    """Address of a contiguous int32 vector of n entries (n < 0: any) on the device."""
+    if t.dtype is not _i32 or t.dim() != 1 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous int32 vector" + ("" if n < 0 else f" of {n} entries"))
+    if t.get_device() != dev:
+        _bad(f"{name} is on {t.device}, expected cuda:{dev}")
+    return t.data_ptr() or _index_ptr(t)
 
 
-def _index(name: str, t, n: Optional[int] = None) -> None:
-    import torch
-    if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
-                          or (n is not None and t.shape[0] != n)):
-        raise ValueError(f"{name} must be a contiguous int32 vector" + ("" if n is None else f" of {n} entries"))
+def _rows(name: str, t, dtype, rows: int, dim: int, dev: int):
+    """(heads, address, token stride, head stride) of a [rows, heads, dim] tensor."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3:
+        _bad(f"{name} must be a {dtype} tensor [{rows}, heads, {dim}] on cuda:{dev}")
+    n, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if n != rows or d != dim or (s2 != 1 and n * heads * d):
+        _bad(f"{name} must be [{rows}, heads, {dim}] with contiguous heads, got {tuple(t.shape)}")
+    return heads, t.data_ptr(), s0, s1
 
 
-def _device(dev):
-    """Context that makes ``dev`` current for the launch (a no-op when it already is)."""
-    import torch
-    _need(dev.type == "cuda", "tensors must be on a CUDA device")
-    return _NULL if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+class _Launch:
+    """Makes the tensors' device current for a call, and a given stream current for its allocations (so
+    that their memory is not handed out again before the stream's work is done)."""
+    __slots__ = ("contexts",)
+
+    def __init__(self, dev: int, stream):
+        self.contexts = []
+        if _cuda_device() != dev:
+            self.contexts.append(torch.cuda.device(dev))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                handle = int(getattr(stream, "cuda_stream", stream))
+                stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+            if stream.device.index != dev:
+                _bad(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
 
 
-def _stream(stream, dev) -> int:
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream(dev).cuda_stream
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+def _elsewhere(dev: int, stream) -> bool:
+    return stream is not None or _cuda_device() != dev
 
 
-def _on_stream(stream, dev):
-    """Context in which outputs are allocated for work on ``stream``, so that their memory is not
-    handed out again before that work is done."""
-    if stream is None:
-        return _NULL
-    import torch
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    return torch.cuda.stream(stream)
-
-
-def _rope(rope_dim: int, rope_theta: float, rope_layout: str, inv_freq, mscale: float):
-    """(skv_rope, the frequency array it points to -- keep it until the call returns)."""
-    _need(rope_layout in _ROPE, f"rope_layout must be one of {sorted(_ROPE)}")
-    if inv_freq is None or rope_dim == 0:
-        return Rope(rope_dim, _ROPE[rope_layout], rope_theta, None, mscale), None
+def _freqs(rope_dim: int, rope_layout: str, inv_freq):
+    """(layout code, address of the frequencies or 0, the array to keep until the call returns)."""
+    layout = _ROPE.get(rope_layout)
+    if layout is None:
+        _bad(f"rope_layout must be one of {sorted(_ROPE)}")
+    if inv_freq is None or rope_dim <= 0:
+        return layout, 0, None
     f = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    _need(f.shape == (rope_dim // 2,), f"inv_freq must hold rope_dim / 2 = {rope_dim // 2} frequencies")
-    return Rope(rope_dim, _ROPE[rope_layout], rope_theta, f.__array_interface__["data"][0], mscale), f
+    if f.ndim != 1 or 2 * f.shape[0] != rope_dim:
+        _bad(f"inv_freq must hold rope_dim / 2 = {rope_dim // 2} frequencies")
+    return layout, f.__array_interface__["data"][0], f
 
 
 def rope_frequencies(rope_dim: int, rope_theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -82,18 +152,17 @@ def rope_frequencies(rope_dim: int, rope_theta: float = 10000.0, scaling: str = 
     stretched, those that turn more than ``high`` times kept, a ramp between; 1 and 32 by default for
     "yarn", which also gives an mscale, 1 and 4 for "bands").  Pass both on to ``rope_apply`` or
     ``paged_kv_append``."""
-    _need(scaling in _ROPE_SCALING, f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    if scaling not in _ROPE_SCALING:
+        _bad(f"scaling must be one of {sorted(_ROPE_SCALING)}")
     lo = 1.0 if low is None else low
     hi = (4.0 if scaling == "bands" else 32.0) if high is None else high
-    f, m = np.zeros(max(1, rope_dim // 2)), ctypes.c_float(1.0)
+    f, m = np.zeros(max(0, rope_dim // 2)), ctypes.c_float(1.0)
     _check(_rope_frequencies(rope_dim, rope_theta, _ROPE_SCALING[scaling], factor, original_context, lo, hi,
                              f.ctypes.data, ctypes.byref(m)), "skv_rope_frequencies")
     return f, float(m.value)
 
 
-def _rows3(name: str, t, rows: int, dim: int) -> None:
-    _need(t.dim() == 3 and t.shape[0] == rows and t.shape[2] == dim and (t.stride(2) == 1 or t.numel() == 0),
-          f"{name} must be [{rows}, heads, {dim}] with contiguous heads, got {tuple(t.shape)}")
+_NO_ROWS = (0, 0, 0, 0)
 
 
 def rope_apply(q, k, positions, *, rope_dim: Optional[int] = None, rope_theta: float = 10000.0,
@@ -104,46 +173,75 @@ def rope_apply(q, k, positions, *, rope_dim: Optional[int] = None, rope_theta: f
     ``rope_dim`` (default D) values of a head turn, the others are copied.  ``inv_freq`` (float64, host)
     replaces rope_theta^(-2p/rope_dim).  ``q_out=q`` / ``k_out=k`` rotates in place; ``inverse`` turns
     back (and takes gradients through the rotation).  Returns (q_out, k_out)."""
-    import torch
+    if torch is None:
+        _init()
     x = q if q is not None else k
-    _need(x is not None, "one of q and k is needed")
-    _need(x.dim() == 3, "q and k are [tokens, heads, head_dim]")
-    dev, tokens, dim, dtype = x.device, x.shape[0], x.shape[2], x.dtype
-    _need(dtype in (torch.bfloat16, torch.float32), "q and k must be bfloat16 or float32")
-    _on(dev, q=q, k=k, positions=positions, q_out=q_out, k_out=k_out)
-    _index("positions", positions, tokens)
-    with _device(dev):
-        with _on_stream(stream, dev):
-            if q is not None and q_out is None:
-                q_out = torch.empty(q.shape, dtype=dtype, device=dev)
-            if k is not None and k_out is None:
-                k_out = torch.empty(k.shape, dtype=dtype, device=dev)
-        args = [None] * 4
-        strides = [(0, 0)] * 4
-        for i, (name, t, like) in enumerate((("q", q, q), ("q_out", q_out, q), ("k", k, k), ("k_out", k_out, k))):
-            if like is None:
-                _need(t is None, f"{name} without its input")
-                continue
-            _rows3(name, t, tokens, dim)
-            _need(t.dtype == dtype and t.shape == like.shape, f"{name} must have the dtype and shape of its input")
-            args[i], strides[i] = t.data_ptr(), t.stride()[:2]
-        desc, keep = _rope(dim if rope_dim is None else rope_dim, rope_theta, rope_layout, inv_freq, mscale)
-        p = RopeParams(*args, *strides, positions.data_ptr(), tokens, 0 if q is None else q.shape[1],
-                       0 if k is None else k.shape[1], dim, F32 if dtype == torch.float32 else BF16, int(inverse), desc)
-        _check(_rope_apply(ctypes.byref(p), _stream(stream, dev)), "skv_rope_apply")
-    del keep
+    if x is None or x.dim() != 3:
+        _bad("q or k is needed, [tokens, heads, head_dim]")
+    dtype = x.dtype
+    if dtype is not _bf16 and dtype is not _f32:
+        _bad("q and k must be bfloat16 or float32")
+    dev = _device_index(x)
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return rope_apply(q, k, positions, rope_dim=rope_dim, rope_theta=rope_theta, rope_layout=rope_layout,
+                              inv_freq=inv_freq, mscale=mscale, inverse=inverse, q_out=q_out, k_out=k_out)
+    tokens, _, dim = x.shape
+    at = _index("positions", positions, tokens, dev)
+    hq = hk = 0
+    qi = qo = ki = ko = _NO_ROWS
+    if q is not None:
+        qi = _rows("q", q, dtype, tokens, dim, dev)
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        qo = _rows("q_out", q_out, dtype, tokens, dim, dev)
+        hq = qi[0]
+    if k is not None:
+        ki = _rows("k", k, dtype, tokens, dim, dev)
+        if k_out is None:
+            k_out = k.new_empty(k.shape)
+        ko = _rows("k_out", k_out, dtype, tokens, dim, dev)
+        hk = ki[0]
+    if qo[0] != hq or ko[0] != hk or (q is None and q_out is not None) or (k is None and k_out is not None):
+        _bad("q_out and k_out must have the shapes of q and k")
+    rope_dim = dim if rope_dim is None else rope_dim
+    layout, freq, keep = _freqs(rope_dim, rope_layout, inv_freq)
+    code = _call_rope(_pack_rope(qi[1], qo[1], ki[1], ko[1], qi[2], qi[3], qo[2], qo[3], ki[2], ki[3], ko[2], ko[3], at,
+                                 tokens, hq, hk, dim, F32 if dtype is _f32 else BF16, 1 if inverse else 0, rope_dim,
+                                 layout, rope_theta, freq, mscale), _raw_stream(dev))
+    if code:
+        raise SkvError(code, "skv_rope_apply")
     return q_out, k_out
 
 
-def _scales(k_cache, k_scale, v_scale, num_pages: int):
+def _caches(k_cache, v_cache, dim: int, num_pages, dev: int):
+    """(dtype code, pages, page size, Hk, page / slot / head strides of K and V) of a pair of caches."""
+    code = _cache_codes.get(k_cache.dtype)
+    if code is None or v_cache.dtype is not k_cache.dtype:
+        _bad("caches must both be bfloat16, float8_e4m3fn or int8")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        _bad("the caches must both be [num_pages, P, Hk, D]")
+    held, page, hk, d = k_cache.shape
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if d != dim or ks[3] != 1 or vs[3] != 1:
+        _bad(f"the caches must be [num_pages, P, Hk, {dim}] with contiguous heads")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        _bad(f"the caches must be on cuda:{dev}")
+    pages = held if num_pages is None else num_pages
+    if not 0 <= pages <= held:
+        _bad("num_pages is more than the cache holds")
+    return code, pages, page, hk, ks, vs
+
+
+def _scales(k_scale, v_scale, pages: int, page: int, hk: int, dev: int) -> int:
     """Tokens that share a scale in the scale tensors [num_pages, blocks per page, Hk] float32."""
-    import torch
-    page, hk = k_cache.shape[1], k_cache.shape[2]
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(t.dim() == 3 and t.dtype == torch.float32 and t.shape[0] >= num_pages and t.shape[2] == hk
-              and t.shape[1] > 0 and page % t.shape[1] == 0 and t.shape[1] == k_scale.shape[1],
-              f"{name} must be float32 [num_pages, blocks per page, {hk}] with whole blocks of tokens")
-    return page // k_scale.shape[1]
+        if t is None or t.dtype is not _f32 or t.dim() != 3 or t.get_device() != dev:
+            _bad(f"{name} must be float32 [num_pages, blocks per page, {hk}] on cuda:{dev}")
+    n, blocks, heads = k_scale.shape
+    if v_scale.shape != k_scale.shape or n < pages or heads != hk or blocks < 1 or page % blocks:
+        _bad(f"k_scale and v_scale must be float32 [num_pages, blocks per page, {hk}] with whole blocks of tokens")
+    return page // blocks
 
 
 def paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices, kv_last_page_len, *, k_scale=None,
@@ -157,61 +255,83 @@ def paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices
     ``v_scale`` float32 [num_pages, P / block, Hk], one scale for each block of tokens and head, which
     the call updates.  ``rope_dim`` > 0 rotates the keys (and ``q`` [rows, Hq, D]) on the way, at the
     tokens' positions or at ``positions``.  Returns q_out (None without q)."""
-    import torch
-    _need(k.dim() == 3 and k_cache.dim() == 4, "k is [rows, Hk, D], the caches [num_pages, P, Hk, D]")
-    dev, rows, hk, dim = k.device, k.shape[0], k.shape[1], k.shape[2]
-    code = _cache_code(k_cache.dtype)
-    _need(code is not None and v_cache.dtype == k_cache.dtype, "caches must both be bfloat16, float8_e4m3fn or int8")
-    _need(k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16, "k and v must be bfloat16")
-    _on(dev, v=v, k_cache=k_cache, v_cache=v_cache, append_indptr=append_indptr, kv_indptr=kv_indptr,
-        kv_indices=kv_indices, kv_last_page_len=kv_last_page_len, k_scale=k_scale, v_scale=v_scale, q=q, q_out=q_out,
-        positions=positions, status=status)
-    _rows3("k", k, rows, dim)
-    _rows3("v", v, rows, dim)
-    _need(v.shape[1] == hk and k_cache.shape[2:] == (hk, dim) and v_cache.shape == k_cache.shape
-          and k_cache.stride(3) == 1 and v_cache.stride(3) == 1, "the caches must be [num_pages, P, Hk, D] like k and v")
+    if torch is None:
+        _init()
+    if k.dim() != 3:
+        _bad("k and v are [rows, Hk, D]")
+    dev = _device_index(k)
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                                   k_scale=k_scale, v_scale=v_scale, kv_scale=kv_scale, q=q, q_out=q_out,
+                                   positions=positions, rope_dim=rope_dim, rope_theta=rope_theta,
+                                   rope_layout=rope_layout, inv_freq=inv_freq, mscale=mscale, num_pages=num_pages,
+                                   status=status)
+    rows, _, dim = k.shape
+    ki, vi = _rows("k", k, _bf16, rows, dim, dev), _rows("v", v, _bf16, rows, dim, dev)
+    code, pages, page, hk, ks, vs = _caches(k_cache, v_cache, dim, num_pages, dev)
+    if ki[0] != hk or vi[0] != hk:
+        _bad(f"k, v and the caches must have the same heads, got {ki[0]}, {vi[0]} and {hk}")
+    if append_indptr.dim() != 1 or append_indptr.shape[0] < 1:
+        _bad("append_indptr must be a contiguous int32 vector")
     batch = append_indptr.shape[0] - 1
-    _index("append_indptr", append_indptr)
-    _index("kv_indptr", kv_indptr, batch + 1)
-    _index("kv_indices", kv_indices)
-    _index("kv_last_page_len", kv_last_page_len, batch)
-    _index("positions", positions, rows)
-    pages = k_cache.shape[0] if num_pages is None else num_pages
-    _need(0 <= pages <= k_cache.shape[0], "num_pages is more than the cache holds")
-    block = 0
+    block, kp, vp, kss, vss = 0, 0, 0, _NO_ROWS, _NO_ROWS
     if k_scale is not None or v_scale is not None:
-        _need(k_scale is not None and v_scale is not None, "k_scale and v_scale come together")
-        block = _scales(k_cache, k_scale, v_scale, pages)
-    with _device(dev):
-        if q is not None:
-            if q_out is None:
-                with _on_stream(stream, dev):
-                    q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-            for name, t in (("q", q), ("q_out", q_out)):
-                _rows3(name, t, rows, dim)
-                _need(t.dtype == torch.bfloat16 and t.shape == q.shape, f"{name} must be bfloat16 [rows, Hq, D]")
-        else:
-            _need(q_out is None, "q_out without q")
-        desc, keep = _rope(rope_dim, rope_theta, rope_layout, inv_freq, mscale)
-        none3 = (0, 0, 0)
-        p = AppendParams(k.data_ptr(), v.data_ptr(), k.stride()[:2], v.stride()[:2], k_cache.data_ptr(),
-                         v_cache.data_ptr(), k_cache.stride()[:3], v_cache.stride()[:3], code, kv_scale, block,
-                         k_scale.data_ptr() if block else None, v_scale.data_ptr() if block else None,
-                         k_scale.stride() if block else none3, v_scale.stride() if block else none3,
-                         append_indptr.data_ptr(), kv_indptr.data_ptr(), _index_ptr(kv_indices),
-                         _index_ptr(kv_last_page_len), None if positions is None else positions.data_ptr(), batch, rows,
-                         pages, k_cache.shape[1], hk, dim, desc, None if q is None else q.data_ptr(),
-                         None if q is None else q_out.data_ptr(), (0, 0) if q is None else q.stride()[:2],
-                         (0, 0) if q is None else q_out.stride()[:2], 0 if q is None else q.shape[1],
-                         None if status is None else status.data_ptr())
-        _check(_kv_append(ctypes.byref(p), _stream(stream, dev)), "skv_paged_kv_append")
-    del keep
+        block = _scales(k_scale, v_scale, pages, page, hk, dev)
+        kp, vp, kss, vss = k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(), v_scale.stride()
+    qi = qo = _NO_ROWS
+    if q is not None:
+        qi = _rows("q", q, _bf16, rows, dim, dev)
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        qo = _rows("q_out", q_out, _bf16, rows, dim, dev)
+    if qo[0] != qi[0] or (q is None and q_out is not None):
+        _bad("q_out must have the shape of q")
+    layout, freq, keep = _freqs(rope_dim, rope_layout, inv_freq)
+    ret = _call_append(_pack_append(
+        ki[1], vi[1], ki[2], ki[3], vi[2], vi[3], k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0],
+        vs[1], vs[2], code, kv_scale, block, kp, vp, kss[0], kss[1], kss[2], vss[0], vss[1], vss[2],
+        _index("append_indptr", append_indptr, batch + 1, dev), _index("kv_indptr", kv_indptr, batch + 1, dev),
+        _index("kv_indices", kv_indices, -1, dev), _index("kv_last_page_len", kv_last_page_len, batch, dev),
+        0 if positions is None else _index("positions", positions, rows, dev), batch, rows, pages, page, hk, dim,
+        rope_dim, layout, rope_theta, freq, mscale, qi[1], qo[1], qi[2], qi[3], qo[2], qo[3], qi[0],
+        0 if status is None else _index("status", status, -1, dev)), _raw_stream(dev))
+    if ret:
+        raise SkvError(ret, "skv_paged_kv_append")
     return q_out
 
 
-def _dev_i32(a, dev):
-    import torch
-    return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype=np.int32))).to(dev)
+def _outputs(q, total_q: int, hq: int, dim: int, o_dtype, o_out, lse_out, dev: int):
+    """(o, its dtype code, lse), allocated unless given."""
+    if o_out is None:
+        dtype = o_dtype or _f32
+        o = q.new_empty((total_q, hq, dim), dtype=dtype)
+    else:
+        o, dtype = o_out, o_out.dtype
+        if tuple(o.shape) != (total_q, hq, dim) or not o.is_contiguous() or o.get_device() != dev:
+            _bad(f"o_out must be contiguous [{total_q}, {hq}, {dim}] on cuda:{dev}")
+    if dtype is not _f32 and dtype is not _bf16:
+        _bad("outputs are float32 or bfloat16")
+    if lse_out is None:
+        lse = q.new_empty((total_q, hq), dtype=_f32)
+    else:
+        lse = lse_out
+        if tuple(lse.shape) != (total_q, hq) or not lse.is_contiguous() or lse.get_device() != dev or lse.dtype is not _f32:
+            _bad(f"lse_out must be contiguous float32 [{total_q}, {hq}] on cuda:{dev}")
+    return o, BF16 if dtype is _bf16 else F32, lse
+
+
+def _workspace(q, plan: Plan, hq: int, dim: int):
+    """(buffer for the plan's split partials, addresses of o_part and lse_part in it)."""
+    n = plan.info.num_partial_rows
+    if n == 0:
+        return None, 0, 0
+    ws = q.new_empty(n * hq * (dim + 1), dtype=_f32)
+    return ws, ws.data_ptr(), ws.data_ptr() + 4 * n * hq * dim
+
+
+def _dev_i32(a, like):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype=np.int32))).to(like.device)
 
 
 def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, kv_indptr_h, kv_indices,
@@ -225,57 +345,52 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
     its last positions and each sees keys up to its own.  Host page-table shape arrays (``*_h``) feed
     the planner; ``plan`` (``plan_paged_scaled`` with the same ``causal``) and device copies ``kv_indptr`` /
     ``kv_last_page_len`` may be kept over the layers of a step.
-    Returns (o, lse, extras) with extras = {"plan", "o_part", "lse_part"}."""
-    import torch
-    _need(q.dim() == 3 and k_cache.dim() == 4, "q is [total_q, Hq, D], the caches [num_pages, P, Hk, D]")
-    dev, total_q, hq, dim = q.device, q.shape[0], q.shape[1], q.shape[2]
-    hk, page = k_cache.shape[2], k_cache.shape[1]
-    code = _cache_code(k_cache.dtype)
-    _need(q.dtype == torch.bfloat16 and q.is_contiguous(), "q must be contiguous bfloat16")
-    _need(code in (E4M3, I8) and v_cache.dtype == k_cache.dtype, "caches must both be float8_e4m3fn or int8")
-    _need(v_cache.shape == k_cache.shape and k_cache.shape[3] == dim and k_cache.stride(3) == 1
-          and v_cache.stride(3) == 1, "the caches must be [num_pages, P, Hk, D] with the head_dim of q")
-    _need(len(qo_indptr_h) > 0 and total_q >= int(qo_indptr_h[-1]), "q has fewer rows than qo_indptr names")
-    pages = k_cache.shape[0] if num_pages is None else num_pages
-    _need(0 <= pages <= k_cache.shape[0], "num_pages is more than the cache holds")
-    block = _scales(k_cache, k_scale, v_scale, pages)
+    Returns (o, lse, extras) with extras = {"plan", "workspace"} (the split partials' buffer)."""
+    if torch is None:
+        _init()
+    if q.dim() != 3:
+        _bad("q is [total_q, Hq, D]")
+    dev = _device_index(q)
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, kv_indptr_h, kv_indices,
+                                          kv_last_page_len_h, sm_scale=sm_scale, causal=causal, policy=policy,
+                                          param=param, split_page_start=split_page_start, o_dtype=o_dtype,
+                                          num_pages=num_pages, kv_indptr=kv_indptr, kv_last_page_len=kv_last_page_len,
+                                          plan=plan, status=status, o_out=o_out, lse_out=lse_out)
+    total_q, hq, dim = q.shape
+    if q.dtype is not _bf16 or not q.is_contiguous():
+        _bad("q must be contiguous bfloat16")
+    code, pages, page, hk, ks, vs = _caches(k_cache, v_cache, dim, num_pages, dev)
+    if code == BF16:
+        _bad("caches must both be float8_e4m3fn or int8")
+    block = _scales(k_scale, v_scale, pages, page, hk, dev)
     batch = len(qo_indptr_h) - 1
-    _on(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, kv_indices=kv_indices,
-        kv_indptr=kv_indptr, kv_last_page_len=kv_last_page_len, status=status, o_out=o_out, lse_out=lse_out)
-    _index("kv_indices", kv_indices)
-    _index("kv_indptr", kv_indptr, batch + 1)
-    _index("kv_last_page_len", kv_last_page_len, batch)
-    for name, t, shape in (("o_out", o_out, (total_q, hq, dim)), ("lse_out", lse_out, (total_q, hq))):
-        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous()), f"{name} must be contiguous {shape}")
-    _need(lse_out is None or lse_out.dtype == torch.float32, "lse_out must be float32")
-    out_dtype = o_out.dtype if o_out is not None else (o_dtype or torch.float32)
-    _need(out_dtype in (torch.float32, torch.bfloat16), "outputs are float32 or bfloat16")
-    with _device(dev), _on_stream(stream, dev):
-        if plan is None:
-            plan = plan_paged_scaled(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, page, hq, hk, dim, causal, policy,
-                                     param, split_page_start)
-        if plan.device is None:
-            plan.to(dev)
-        if kv_indptr is None:
-            kv_indptr = _dev_i32(kv_indptr_h, dev)
-        if kv_last_page_len is None:
-            kv_last_page_len = _dev_i32(kv_last_page_len_h, dev)
-        o = torch.empty(total_q, hq, dim, dtype=out_dtype, device=dev) if o_out is None else o_out
-        lse = torch.empty(total_q, hq, dtype=torch.float32, device=dev) if lse_out is None else lse_out
-        n_part = plan.info.num_partial_rows
-        o_part = torch.empty(n_part, hq, dim, dtype=torch.float32, device=dev) if n_part else None
-        lse_part = torch.empty(n_part, hq, dtype=torch.float32, device=dev) if n_part else None
-        base = PagedParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_cache.stride()[:3],
-                           v_cache.stride()[:3], kv_indptr.data_ptr(), _index_ptr(kv_indices),
-                           _index_ptr(kv_last_page_len), batch, total_q, pages, page, hq, hk, dim,
-                           dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(),
-                           BF16 if out_dtype == torch.bfloat16 else F32, lse.data_ptr(),
-                           o_part.data_ptr() if n_part else None, lse_part.data_ptr() if n_part else None,
-                           None if status is None else status.data_ptr(), code, 1.0)
-        p = PagedScaledParams(base, k_scale.data_ptr(), v_scale.data_ptr(), k_scale.stride(), v_scale.stride(), block)
-        _check(_scaled_fwd(ctypes.byref(p), plan.device.data_ptr(), ctypes.byref(plan.info), _stream(stream, dev)),
-               "skv_paged_attn_scaled_fwd")
-    return o, lse, {"plan": plan, "o_part": o_part, "lse_part": lse_part}
+    if batch < 0 or total_q < qo_indptr_h[batch]:
+        _bad("q has fewer rows than qo_indptr names")
+    if plan is None:
+        plan = plan_paged_scaled(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, page, hq, hk, dim, causal, policy, param,
+                                 split_page_start)
+    if plan.device is None:
+        plan.to(q.device)
+    if kv_indptr is None:
+        kv_indptr = _dev_i32(kv_indptr_h, q)
+    if kv_last_page_len is None:
+        kv_last_page_len = _dev_i32(kv_last_page_len_h, q)
+    o, o_code, lse = _outputs(q, total_q, hq, dim, o_dtype, o_out, lse_out, dev)
+    ws, o_part, lse_part = _workspace(q, plan, hq, dim)
+    kss, vss = k_scale.stride(), v_scale.stride()
+    ret = _call_scaled(_pack_scaled(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+        _index("kv_indptr", kv_indptr, batch + 1, dev), _index("kv_indices", kv_indices, -1, dev),
+        _index("kv_last_page_len", kv_last_page_len, batch, dev), batch, total_q, pages, page, hq, hk, dim,
+        dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(), o_code, lse.data_ptr(), o_part, lse_part,
+        0 if status is None else _index("status", status, -1, dev), code, 1.0, k_scale.data_ptr(), v_scale.data_ptr(),
+        kss[0], kss[1], kss[2], vss[0], vss[1], vss[2], block), _index("plan", plan.device, -1, dev),
+        ctypes.addressof(plan.info), _raw_stream(dev))
+    if ret:
+        raise SkvError(ret, "skv_paged_attn_scaled_fwd")
+    return o, lse, {"plan": plan, "workspace": ws}
 
 
 def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = True, sm_scale: Optional[float] = None,
@@ -285,41 +400,38 @@ def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = T
     (default: the same rows).  ``causal``: its query tokens are its last positions.  ``plan``
     (``plan_prompt`` with the same ``causal``) may be kept over the layers of a step.  Rows of outputs given as
     ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
-    Returns (o, lse, extras) with extras = {"plan", "o_part", "lse_part"}."""
-    import torch
-    _need(q.dim() == 3 and k.dim() == 3, "q is [total_q, Hq, D], k and v are [total_kv, Hk, D]")
-    dev, total_q, hq, dim = q.device, q.shape[0], q.shape[1], q.shape[2]
-    total_kv, hk = k.shape[0], k.shape[1]
-    _need(q.dtype == torch.bfloat16 and k.dtype == torch.bfloat16 and v.dtype == torch.bfloat16,
-          "q, k and v must be bfloat16")
-    _rows3("q", q, total_q, dim)
-    _rows3("k", k, total_kv, dim)
-    _rows3("v", v, total_kv, dim)
-    _need(v.shape[1] == hk, "k and v must have the same heads")
-    _on(dev, k=k, v=v, status=status, o_out=o_out, lse_out=lse_out)
-    _need(len(qo_indptr_h) > 0 and total_q >= int(qo_indptr_h[-1]), "q has fewer rows than qo_indptr names")
-    _need(total_kv >= int((qo_indptr_h if kv_indptr_h is None else kv_indptr_h)[-1]),
-          "k and v have fewer rows than kv_indptr names")
-    for name, t, shape in (("o_out", o_out, (total_q, hq, dim)), ("lse_out", lse_out, (total_q, hq))):
-        _need(t is None or (tuple(t.shape) == shape and t.is_contiguous()), f"{name} must be contiguous {shape}")
-    _need(lse_out is None or lse_out.dtype == torch.float32, "lse_out must be float32")
-    out_dtype = o_out.dtype if o_out is not None else (o_dtype or torch.float32)
-    _need(out_dtype in (torch.float32, torch.bfloat16), "outputs are float32 or bfloat16")
-    with _device(dev), _on_stream(stream, dev):
-        if plan is None:
-            plan = plan_prompt(qo_indptr_h, kv_indptr_h, hq, hk, dim, causal)
-        if plan.device is None:
-            plan.to(dev)
-        o = torch.empty(total_q, hq, dim, dtype=out_dtype, device=dev) if o_out is None else o_out
-        lse = torch.empty(total_q, hq, dtype=torch.float32, device=dev) if lse_out is None else lse_out
-        n_part = plan.info.num_partial_rows
-        o_part = torch.empty(n_part, hq, dim, dtype=torch.float32, device=dev) if n_part else None
-        lse_part = torch.empty(n_part, hq, dtype=torch.float32, device=dev) if n_part else None
-        p = PromptParams(q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride()[:2], k.stride()[:2], v.stride()[:2], total_q,
-                         total_kv, hq, hk, dim, dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(),
-                         BF16 if out_dtype == torch.bfloat16 else F32, lse.data_ptr(),
-                         o_part.data_ptr() if n_part else None, lse_part.data_ptr() if n_part else None,
-                         None if status is None else status.data_ptr())
-        _check(_prompt_fwd(ctypes.byref(p), plan.device.data_ptr(), ctypes.byref(plan.info), _stream(stream, dev)),
-               "skv_prompt_attn_fwd")
-    return o, lse, {"plan": plan, "o_part": o_part, "lse_part": lse_part}
+    Returns (o, lse, extras) with extras = {"plan", "workspace"} (the partials' buffer)."""
+    if torch is None:
+        _init()
+    if q.dim() != 3 or k.dim() != 3:
+        _bad("q is [total_q, Hq, D], k and v are [total_kv, Hk, D]")
+    dev = _device_index(q)
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h, causal=causal, sm_scale=sm_scale,
+                                    o_dtype=o_dtype, plan=plan, status=status, o_out=o_out, lse_out=lse_out)
+    total_q, hq, dim = q.shape
+    total_kv = k.shape[0]
+    qi, ki = _rows("q", q, _bf16, total_q, dim, dev), _rows("k", k, _bf16, total_kv, dim, dev)
+    vi = _rows("v", v, _bf16, total_kv, dim, dev)
+    hk = ki[0]
+    if vi[0] != hk:
+        _bad("k and v must have the same heads")
+    if len(qo_indptr_h) < 1 or total_q < qo_indptr_h[-1]:
+        _bad("q has fewer rows than qo_indptr names")
+    if total_kv < (qo_indptr_h if kv_indptr_h is None else kv_indptr_h)[-1]:
+        _bad("k and v have fewer rows than kv_indptr names")
+    if plan is None:
+        plan = plan_prompt(qo_indptr_h, kv_indptr_h, hq, hk, dim, causal)
+    if plan.device is None:
+        plan.to(q.device)
+    o, o_code, lse = _outputs(q, total_q, hq, dim, o_dtype, o_out, lse_out, dev)
+    ws, o_part, lse_part = _workspace(q, plan, hq, dim)
+    ret = _call_prompt(_pack_prompt(
+        qi[1], ki[1], vi[1], qi[2], qi[3], ki[2], ki[3], vi[2], vi[3], total_q, total_kv, hq, hk, dim,
+        dim ** -0.5 if sm_scale is None else sm_scale, o.data_ptr(), o_code, lse.data_ptr(), o_part, lse_part,
+        0 if status is None else _index("status", status, -1, dev)), _index("plan", plan.device, -1, dev),
+        ctypes.addressof(plan.info), _raw_stream(dev))
+    if ret:
+        raise SkvError(ret, "skv_prompt_attn_fwd")
+    return o, lse, {"plan": plan, "workspace": ws}

@@ -7,10 +7,15 @@
 //
 // Bound by HBM: 2 Hk D bytes per token.  One CTA takes `hc` KV heads (the largest of 8, 4, 2, 1 that
 // divides Hk) of a slice of the batch's tokens (persistent, slices cut equal by the planner), so a
-// token's rows of those heads are read together.  Four producer warps fill a ring of shared-memory
-// stages with cp.async (any page size, any 16-byte strides; rows past the end are zero-filled
-// without reading); eight consumer warps each own one head and 32 tokens of a stage and keep their
-// own running maximum, sum and O, merged across the warps of a head when a work item ends.
+// token's rows of those heads are read together.  Eight consumer warps each own one head and 32
+// tokens of a shared-memory stage and keep their own running maximum, sum and O, merged across the
+// warps of a head when a work item ends.  The ring of stages is filled
+//   - by TMA (one warp, one box of min(page, tile) slots x hc heads per page and tensor) where the
+//     page size divides the tile or is a multiple of it, is a multiple of 8, and blocks are whole
+//     groups of 8 tokens (one scale per group and head is staged);
+//   - else by cp.async from four warps (any page size, block size and 16-byte strides; one scale per
+//     token and head).  Measured on the 64-request 64/8-head e4m3 decode, pages of 16: 225 us
+//     against 106 us by TMA: address arithmetic for 4096 copies a stage holds the ring back.
 //
 // Decode has few query rows per KV head (R = group x query tokens <= 16), far below the 128 rows of
 // the tcgen05 shapes, and each code needs widening in registers anyway, so the products are
@@ -27,10 +32,13 @@
 // [2^14, 2^15): exact for every element of at least 2^-31 of the row's largest).  Weights are formed as
 // p * (vs / vref), vref the largest vs of the 32 tokens, in f16 (11 bits; the maximum is raised
 // once a score passes it by 2^8, so p <= 2^8), and the partial product is scaled by vref in fp32.
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <string.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "tc_ptx.cuh"
 
@@ -39,8 +47,11 @@ namespace skv {
 namespace {
 
 constexpr int kConsumers = 8;                 // warps
-constexpr int kProducers = 4;                 // warps
-constexpr int kThreads = 32 * (kConsumers + kProducers);
+constexpr int kCopyWarps = 4;                 // producer warps (with TMA the last three only exit)
+constexpr int kThreads = 32 * (kConsumers + kCopyWarps);
+// Registers: 384 threads start with 168; the consumers take 208, the producers' warpgroup gives up to 88.
+constexpr int kConsumerRegs = 208, kProducerRegs = 88;
+static_assert(256 * kConsumerRegs + 128 * kProducerRegs <= kThreads * 168, "the split fits the launch's registers");
 constexpr int kWarpTokens = 32;               // tokens of a stage that one consumer warp takes
 constexpr float kRaise = 8.f;
 
@@ -57,10 +68,12 @@ struct Smem {
   static constexpr int misc = bars + 2 * stages * 8;
   static constexpr int total = misc + 16;
 };
-static_assert(Smem<128>::total <= 232448 && Smem<64>::total <= 232448, "227 KB opt-in shared memory");
+static_assert(Smem<128>::stage % 1024 == 0 && Smem<64>::stage % 1024 == 0, "swizzled boxes start on 1024 bytes");
+static_assert(Smem<128>::total + 1024 <= 232448 && Smem<64>::total + 1024 <= 232448, "227 KB opt-in shared memory");
 
 struct SArgs {
   const __nv_bfloat16* q;
+  int box_log2;       // TMA: slots of a box
   const uint8_t* k;
   const uint8_t* v;
   const float* ks;
@@ -182,9 +195,12 @@ __device__ __forceinline__ Range item_range(const SArgs& a, const WorkItem& w, i
   return r;
 }
 
-template <bool I8, int D, bool WIDE, typename OutT>
-__global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_constant__ SArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+template <bool I8, int D, bool WIDE, bool TMA, typename OutT>
+__global__ void __launch_bounds__(kThreads, 1)
+gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ SArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   using S = Smem<D>;
   constexpr int kChunks = D / 16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -196,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
   auto empty_bar = [&](int s) { return bar0 + 8u * (S::stages + s); };
   if (tid == 0) {
     for (int s = 0; s < S::stages; ++s) {
-      tc::mbar_init(full_bar(s), 32 * kProducers);
+      tc::mbar_init(full_bar(s), TMA ? 33 : 32 * kCopyWarps);  // TMA: its transaction and 32 lanes' scales
       tc::mbar_init(empty_bar(s), kConsumers);
     }
     *abort_flag = 0;
@@ -210,78 +226,145 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
   const int w_begin = a.cta_indptr[cta], w_end = a.cta_indptr[cta + 1];
 
   if (warp >= kConsumers) {
-    // ================================================================================ producers
-    const int pw = warp - kConsumers;
-    const int mine = tile_tokens / kProducers;  // 8, 16, 32 or 64 tokens of a tile for this warp
-    int it = 0;
-    bool ok = true;
-    for (int wi = w_begin; wi < w_end && ok; ++wi) {
-      const WorkItem w = a.work[wi];
-      const Range rg = item_range(a, w, tile_tokens);
-      const int32_t* ids = a.kv_indices + a.kv_indptr[w.r];
-      // page ids of this warp's tokens, one tile ahead of their use
-      int next[2];
-      auto fetch_ids = [&](int tile) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int tok = rg.t0 + tile * tile_tokens + pw * mine + b * 32 + lane;
-          next[b] = (b * 32 + lane < mine && tok < rg.t1) ? __ldg(ids + tok / a.page_size) : 0;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
+    if constexpr (TMA) {
+      if (warp != kConsumers) return;
+      // ============================================================================= TMA producer
+      // Lane i stages the scales of 8-token group i / hc for head i % hc; the lanes of head 0 whose
+      // group begins a box issue that box's K and V.
+      const int first = (lane >> a.hc_log2) * 8, hh = lane & (hc - 1);
+      const int box = 1 << a.box_log2;
+      const bool issues = hh == 0 && (first & (box - 1)) == 0;
+      const uint64_t pol = tc::policy_evict_first();
+      int it = 0;
+      bool ok = true;
+      if (lane == 0) {
+        tc::prefetch_tmap(&kmap);
+        tc::prefetch_tmap(&vmap);
+      }
+      for (int wi = w_begin; wi < w_end && ok; ++wi) {
+        const WorkItem w = a.work[wi];
+        const Range rg = item_range(a, w, tile_tokens);
+        const int32_t* ids = a.kv_indices + a.kv_indptr[w.r];
+        auto page_of = [&](int tile) {  // page id of this lane's group, read one tile ahead of its use
+          const int tok = rg.t0 + tile * tile_tokens + first;
+          return tile < rg.tiles && tok < rg.t1 ? __ldg(ids + tok / a.page_size) : 0;
+        };
+        int next = page_of(0);
+        for (int tile = 0; tile < rg.tiles; ++tile, ++it) {
+          const int st = it % S::stages, page = next;
+          const int tok = rg.t0 + tile * tile_tokens + first, slot = tok % a.page_size;
+          const bool some = tok < rg.t1;
+          const bool sound = (unsigned)page < (unsigned)a.num_pages;
+          if (some && !sound && hh == 0) report(a.status, SKV_DEV_PAGE_OOB);
+          next = page_of(tile + 1);
+          if (it >= S::stages) ok = tc::mbar_wait(empty_bar(st), ((it / S::stages) + 1) & 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv, kss = vst + S::kv, vss = kss + S::scales;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issues && some));
+          if (lane == 0) tc::mbar_arrive_expect_tx(full_bar(st), 2 * boxes * (uint32_t)((box * D) << a.hc_log2));
+          __syncwarp();
+          if (issues && some) {  // an id out of range reads as zeros
+            const uint32_t at = (uint32_t)(first * D) << a.hc_log2;
+            tc::tma_load_4d(kst + at, &kmap, full_bar(st), 0, slot, h0, page, pol);
+            tc::tma_load_4d(vst + at, &vmap, full_bar(st), 0, slot, h0, page, pol);
+          }
+          const bool valid = some && sound;
+          const int blk = slot / a.block_tokens;
+          const int64_t so = (int64_t)(valid ? page : 0) * a.ks0 + (int64_t)blk * a.ks1 + (int64_t)(h0 + hh) * a.ks2;
+          const int64_t vo = (int64_t)(valid ? page : 0) * a.vs0 + (int64_t)blk * a.vs1 + (int64_t)(h0 + hh) * a.vs2;
+          const uint32_t dst = (uint32_t)((hh * (tile_tokens >> 3) + (first >> 3)) * 4);
+          cp4(kss + dst, a.ks + (valid ? so : 0), valid);
+          cp4(vss + dst, a.vs + (valid ? vo : 0), valid);
+          cp_arrive(full_bar(st));
         }
-      };
-      if (rg.tiles > 0) fetch_ids(0);
-      for (int tile = 0; tile < rg.tiles; ++tile, ++it) {
-        const int st = it % S::stages;
-        int id[2] = {next[0], next[1]};
-        if (tile + 1 < rg.tiles) fetch_ids(tile + 1);
-        if (it >= S::stages) ok = tc::mbar_wait(empty_bar(st), ((it / S::stages) + 1) & 1, abort_flag, a.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv, kss = vst + S::kv, vss = kss + S::scales;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int n = min(32, mine - b * 32);
-          if (n <= 0) break;
-          const int first = pw * mine + b * 32;                       // tile-relative token of lane 0
-          const int tok = rg.t0 + tile * tile_tokens + first + lane;
-          bool valid = lane < n && tok < rg.t1;
-          if (valid && (unsigned)id[b] >= (unsigned)a.num_pages) {
-            report(a.status, SKV_DEV_PAGE_OOB);
-            valid = false;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (!ok && lane == 0) {  // boxes in flight may still be landing: wait for them (bounded)
+        for (int t = max(0, it - S::stages); t < it; ++t) {
+          const uint64_t t_start = tc::globaltimer_ns();
+          while (!tc::mbar_try_wait(full_bar(t % S::stages), (t / S::stages) & 1) &&
+                 tc::globaltimer_ns() - t_start < 20000000ull) {
           }
-          const int64_t page = valid ? id[b] : 0;
-          const int slot = valid ? tok % a.page_size : 0, blk = slot / a.block_tokens;
-          const int64_t ko = valid ? page * a.k0 + slot * a.k1 : -1;  // -1: zero-filled
-          const int64_t vo = page * a.v0 + slot * a.v1;
-          const int64_t kso = page * a.ks0 + blk * a.ks1, vso = page * a.vs0 + blk * a.vs1;
-          const int copies = (n << a.hc_log2) * kChunks;              // a multiple of 32
-#pragma unroll 4
-          for (int x = lane; x < copies; x += 32) {
-            const int row = x / kChunks, c = x % kChunks, tl = row >> a.hc_log2, h = row & (hc - 1);
-            const int64_t kx = __shfl_sync(0xffffffffu, ko, tl), vx = __shfl_sync(0xffffffffu, vo, tl);
-            const int rt = first + tl;
-            const uint32_t dst = (uint32_t)((h * tile_tokens + rt) * D + ((c ^ swizzle<D>(rt)) << 4));
-            cp16(kst + dst, a.k + (kx < 0 ? 0 : kx + (int64_t)(h0 + h) * a.k2 + c * 16), kx >= 0);
-            cp16(vst + dst, a.v + (kx < 0 ? 0 : vx + (int64_t)(h0 + h) * a.v2 + c * 16), kx >= 0);
+        }
+      }
+      return;
+    } else {
+      // ======================================================================== cp.async producers
+      const int pw = warp - kConsumers;
+      const int mine = tile_tokens / kCopyWarps;  // 8, 16, 32 or 64 tokens of a tile for this warp
+      int it = 0;
+      bool ok = true;
+      for (int wi = w_begin; wi < w_end && ok; ++wi) {
+        const WorkItem w = a.work[wi];
+        const Range rg = item_range(a, w, tile_tokens);
+        const int32_t* ids = a.kv_indices + a.kv_indptr[w.r];
+        // page ids of this warp's tokens, one tile ahead of their use
+        int next[2];
+        auto fetch_ids = [&](int tile) {
+  #pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int tok = rg.t0 + tile * tile_tokens + pw * mine + b * 32 + lane;
+            next[b] = (b * 32 + lane < mine && tok < rg.t1) ? __ldg(ids + tok / a.page_size) : 0;
           }
-          const int pairs = n << a.hc_log2;
-          for (int x0 = 0; x0 < pairs; x0 += 32) {
-            const int x = x0 + lane, tl = x >> a.hc_log2, h = x & (hc - 1);
-            const int64_t kx = __shfl_sync(0xffffffffu, ko, tl & 31);
-            const int64_t sk = __shfl_sync(0xffffffffu, kso, tl & 31), sv = __shfl_sync(0xffffffffu, vso, tl & 31);
-            if (x < pairs) {
-              const uint32_t dst = (uint32_t)((h * tile_tokens + first + tl) * 4);
-              cp4(kss + dst, a.ks + (kx < 0 ? 0 : sk + (int64_t)(h0 + h) * a.ks2), kx >= 0);
-              cp4(vss + dst, a.vs + (kx < 0 ? 0 : sv + (int64_t)(h0 + h) * a.vs2), kx >= 0);
+        };
+        if (rg.tiles > 0) fetch_ids(0);
+        for (int tile = 0; tile < rg.tiles; ++tile, ++it) {
+          const int st = it % S::stages;
+          int id[2] = {next[0], next[1]};
+          if (tile + 1 < rg.tiles) fetch_ids(tile + 1);
+          if (it >= S::stages) ok = tc::mbar_wait(empty_bar(st), ((it / S::stages) + 1) & 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv, kss = vst + S::kv, vss = kss + S::scales;
+  #pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int n = min(32, mine - b * 32);
+            if (n <= 0) break;
+            const int first = pw * mine + b * 32;                       // tile-relative token of lane 0
+            const int tok = rg.t0 + tile * tile_tokens + first + lane;
+            bool valid = lane < n && tok < rg.t1;
+            if (valid && (unsigned)id[b] >= (unsigned)a.num_pages) {
+              report(a.status, SKV_DEV_PAGE_OOB);
+              valid = false;
+            }
+            const int64_t page = valid ? id[b] : 0;
+            const int slot = valid ? tok % a.page_size : 0, blk = slot / a.block_tokens;
+            const int64_t ko = valid ? page * a.k0 + slot * a.k1 : -1;  // -1: zero-filled
+            const int64_t vo = page * a.v0 + slot * a.v1;
+            const int64_t kso = page * a.ks0 + blk * a.ks1, vso = page * a.vs0 + blk * a.vs1;
+            const int copies = (n << a.hc_log2) * kChunks;              // a multiple of 32
+  #pragma unroll 4
+            for (int x = lane; x < copies; x += 32) {
+              const int row = x / kChunks, c = x % kChunks, tl = row >> a.hc_log2, h = row & (hc - 1);
+              const int64_t kx = __shfl_sync(0xffffffffu, ko, tl), vx = __shfl_sync(0xffffffffu, vo, tl);
+              const int rt = first + tl;
+              const uint32_t dst = (uint32_t)((h * tile_tokens + rt) * D + ((c ^ swizzle<D>(rt)) << 4));
+              cp16(kst + dst, a.k + (kx < 0 ? 0 : kx + (int64_t)(h0 + h) * a.k2 + c * 16), kx >= 0);
+              cp16(vst + dst, a.v + (kx < 0 ? 0 : vx + (int64_t)(h0 + h) * a.v2 + c * 16), kx >= 0);
+            }
+            const int pairs = n << a.hc_log2;
+            for (int x0 = 0; x0 < pairs; x0 += 32) {
+              const int x = x0 + lane, tl = x >> a.hc_log2, h = x & (hc - 1);
+              const int64_t kx = __shfl_sync(0xffffffffu, ko, tl & 31);
+              const int64_t sk = __shfl_sync(0xffffffffu, kso, tl & 31), sv = __shfl_sync(0xffffffffu, vso, tl & 31);
+              if (x < pairs) {
+                const uint32_t dst = (uint32_t)((h * tile_tokens + first + tl) * 4);
+                cp4(kss + dst, a.ks + (kx < 0 ? 0 : sk + (int64_t)(h0 + h) * a.ks2), kx >= 0);
+                cp4(vss + dst, a.vs + (kx < 0 ? 0 : sv + (int64_t)(h0 + h) * a.vs2), kx >= 0);
+              }
             }
           }
+          cp_arrive(full_bar(st));
         }
-        cp_arrive(full_bar(st));
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      return;
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    return;
   }
 
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
   // ================================================================================== consumers
   const int g = lane >> 2, t = lane & 3;
   const int h = warp & (hc - 1), sub = warp >> a.hc_log2, subs = kConsumers >> a.hc_log2;
@@ -289,6 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
   constexpr int kKSteps = D / 16;      // k-steps of Q . K^T
   constexpr int kDims = D / 8;         // dims of O each lane column covers (n-tiles of P . V)
   constexpr int kRowSets = WIDE ? 2 : 1;
+  // byte offset of the warp's 8-token groups in K (and V) of a stage, and of its scales
+  uint32_t group_at[4];
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int rt = sub * kWarpTokens + 8 * n;
+    const int in = rt & ((1 << a.box_log2) - 1), box = rt >> a.box_log2;  // TMA: [box][head][slot]
+    group_at[n] = (uint32_t)((TMA ? (((box << a.hc_log2) + h) << a.box_log2) + in : h * tile_tokens + rt) * D);
+  }
+  const uint32_t scale_at = 4u * (TMA ? h * (tile_tokens >> 3) + sub * 4 : h * tile_tokens + sub * kWarpTokens);
   int it = 0;
   bool ok = true;
   for (int wi = w_begin; wi < w_end; ++wi) {
@@ -362,17 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
       ok = tc::mbar_wait(full_bar(st), (it / S::stages) & 1, abort_flag, a.status) && ok;
       const int tb = rg.t0 + tile * tile_tokens + sub * kWarpTokens;  // first token of this warp
       if (ok && tb < rg.t1) {
-        const int rt0 = sub * kWarpTokens;
-        const uint32_t kst = sbase + st * S::stage + (uint32_t)((h * tile_tokens + rt0) * D), vst = kst + S::kv;
-        const uint32_t kss = sbase + st * S::stage + 2 * S::kv + (uint32_t)((h * tile_tokens + rt0) * 4);
-        const uint32_t vss = kss + S::scales;
+        const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv;
+        const uint32_t kss = sbase + st * S::stage + 2 * S::kv + scale_at, vss = kss + S::scales;
         // ---- scores: 4 tiles of 8 tokens
         float s[4][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-          const int tok = 8 * n + col_token<D>(g);
-          const uint32_t row = kst + tok * D;
+          const int tok = col_token<D>(g);
+          const uint32_t row = kst + group_at[n] + tok * D;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
             const uint4 kw = lds128(row + (((4 * j + t) ^ swizzle<D>(tok)) << 4));
@@ -392,9 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
         const bool masked = tb + kWarpTokens > all_see;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const float k0 = lds_f(kss + (8 * n + ta) * 4), k1 = lds_f(kss + (8 * n + tc1) * 4);
-          vsc[n][0] = lds_f(vss + (8 * n + ta) * 4);
-          vsc[n][1] = lds_f(vss + (8 * n + tc1) * 4);
+          float k0, k1;
+          if constexpr (TMA) {  // one scale for the 8 tokens
+            k0 = k1 = lds_f(kss + 4 * n);
+            vsc[n][0] = vsc[n][1] = lds_f(vss + 4 * n);
+          } else {
+            k0 = lds_f(kss + (8 * n + ta) * 4);
+            k1 = lds_f(kss + (8 * n + tc1) * 4);
+            vsc[n][0] = lds_f(vss + (8 * n + ta) * 4);
+            vsc[n][1] = lds_f(vss + (8 * n + tc1) * 4);
+          }
           vref = fmaxf(vref, fmaxf(vsc[n][0], vsc[n][1]));
 #pragma unroll
           for (int r = 0; r < kRowSets; ++r) {
@@ -407,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
             mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
           }
         }
-        vref = quad_max(vref);
+        if constexpr (!TMA) vref = quad_max(vref);
         const float rv = vref > 0.f ? 1.f / vref : 0.f;
         bool raise = false;
 #pragma unroll
@@ -452,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
         for (int n = 0; n < 4; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int tok = 8 * n + (e ? tc1 : ta);
-            const uint32_t row = vst + tok * D;
+            const int tok = e ? tc1 : ta;
+            const uint32_t row = vst + group_at[n] + tok * D;
             if constexpr (D == 128) {
               const uint4 v = lds128(row + ((col_token<D>(g) ^ swizzle<D>(tok)) << 4));
               vw[n][e][0] = v.x;
@@ -466,6 +563,15 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
               vw[n][e][1] = v.y;
             }
           }
+        if (TMA && tb + kWarpTokens > rg.t1) {  // slots past the end hold anything: 0 x NaN is not 0
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (tb + 8 * n + (e ? tc1 : ta) >= rg.t1)
+#pragma unroll
+                for (int q = 0; q < kWords; ++q) vw[n][e][q] = 0u;
+        }
 #pragma unroll
         for (int q = 0; q < kWords; ++q) {
           uint32_t b[4][4];  // [8-token group][dim]: pairs of tokens
@@ -575,22 +681,65 @@ __global__ void __launch_bounds__(kThreads, 1) gqa_scaled_kernel(const __grid_co
   }
 }
 
-template <bool I8, int D, bool WIDE, typename OutT>
-int launch_s(const SArgs& a, int ctas, cudaStream_t s) {
+struct Maps {
+  CUtensorMap k, v;
+};
+
+template <bool I8, int D, bool WIDE, bool TMA, typename OutT>
+int launch_s(const Maps& m, const SArgs& a, int ctas, cudaStream_t s) {
   static DeviceSmemAttr attr;
-  const int smem = Smem<D>::total;
-  if (const int e = attr.ensure(reinterpret_cast<const void*>(gqa_scaled_kernel<I8, D, WIDE, OutT>), smem)) return e;
-  gqa_scaled_kernel<I8, D, WIDE, OutT><<<ctas * a.head_groups * a.row_groups, kThreads, smem, s>>>(a);
+  const int smem = Smem<D>::total + 1024;
+  const auto kernel = gqa_scaled_kernel<I8, D, WIDE, TMA, OutT>;
+  if (const int e = attr.ensure(reinterpret_cast<const void*>(kernel), smem)) return e;
+  kernel<<<ctas * a.head_groups * a.row_groups, kThreads, smem, s>>>(m.k, m.v, a);
   return (int)cudaGetLastError();
 }
 template <bool I8, int D, bool WIDE>
-int launch_o(const SArgs& a, int ctas, int o_dtype, cudaStream_t s) {
-  return o_dtype == SKV_BF16 ? launch_s<I8, D, WIDE, __nv_bfloat16>(a, ctas, s) : launch_s<I8, D, WIDE, float>(a, ctas, s);
+int launch_o(const Maps& m, const SArgs& a, int ctas, bool tma, int o_dtype, cudaStream_t s) {
+  if (o_dtype == SKV_BF16)
+    return tma ? launch_s<I8, D, WIDE, true, __nv_bfloat16>(m, a, ctas, s)
+               : launch_s<I8, D, WIDE, false, __nv_bfloat16>(m, a, ctas, s);
+  return tma ? launch_s<I8, D, WIDE, true, float>(m, a, ctas, s) : launch_s<I8, D, WIDE, false, float>(m, a, ctas, s);
 }
 template <bool I8>
-int launch_d(const SArgs& a, int ctas, int head_dim, bool wide, int o_dtype, cudaStream_t s) {
-  if (head_dim == 128) return wide ? launch_o<I8, 128, true>(a, ctas, o_dtype, s) : launch_o<I8, 128, false>(a, ctas, o_dtype, s);
-  return wide ? launch_o<I8, 64, true>(a, ctas, o_dtype, s) : launch_o<I8, 64, false>(a, ctas, o_dtype, s);
+int launch_d(const Maps& m, const SArgs& a, int ctas, int head_dim, bool wide, bool tma, int o_dtype, cudaStream_t s) {
+  if (head_dim == 128)
+    return wide ? launch_o<I8, 128, true>(m, a, ctas, tma, o_dtype, s)
+                : launch_o<I8, 128, false>(m, a, ctas, tma, o_dtype, s);
+  return wide ? launch_o<I8, 64, true>(m, a, ctas, tma, o_dtype, s)
+              : launch_o<I8, 64, false>(m, a, ctas, tma, o_dtype, s);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Codes [page, slot, head, D] with caller strides (bytes); boxes of `box` slots x `hc` heads of one
+// page, swizzled as the consumers read them (128-byte rows: by token % 8; 64-byte rows: token / 2 % 4).
+bool cache_map(CUtensorMap* m, const void* base, const skv_paged_params& p, const int64_t* stride, int box, int hc) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.head_dim, (cuuint64_t)p.page_size, (cuuint64_t)p.num_kv_heads,
+                              (cuuint64_t)std::max(1, p.num_pages)};
+  cuuint64_t st[3];  // slot, head, page; a dimension of one entry never uses its stride
+  st[0] = p.page_size > 1 ? (cuuint64_t)stride[1] : (cuuint64_t)p.head_dim;
+  st[1] = p.num_kv_heads > 1 ? (cuuint64_t)stride[2] : (cuuint64_t)p.head_dim;
+  st[2] = p.num_pages > 1 ? (cuuint64_t)stride[0] : (cuuint64_t)p.head_dim;
+  for (cuuint64_t x : st)
+    if (x == 0 || x >= (1ull << 40)) return false;
+  const cuuint32_t bx[4] = {(cuuint32_t)p.head_dim, (cuuint32_t)box, (cuuint32_t)hc, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, st, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, p.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -655,8 +804,17 @@ int launch_gqa_scaled(const skv_paged_scaled_params& sp, const WorkItem* work, c
   a.lse_part = p.lse_part;
   a.status = p.status;
   const bool wide = q_tile * a.g > 8;
-  return p.kv_dtype == SKV_I8 ? launch_d<true>(a, num_ctas, p.head_dim, wide, p.o_dtype, s)
-                              : launch_d<false>(a, num_ctas, p.head_dim, wide, p.o_dtype, s);
+  // TMA where a tile is whole boxes of one page each and every 8-token group lies in one block; a box
+  // takes `tile` or `page_size` slots (both powers of two then)
+  const int hc = 1 << a.hc_log2, tile = kConsumers * kWarpTokens / hc, box = std::min(p.page_size, tile);
+  Maps m;
+  memset(&m, 0, sizeof(m));
+  bool tma = p.page_size % 8 == 0 && sp.block_tokens % 8 == 0 && tile % box == 0 && p.page_size % box == 0;
+  tma = tma && cache_map(&m.k, p.k_cache, p, p.k_stride, box, hc) && cache_map(&m.v, p.v_cache, p, p.v_stride, box, hc);
+  a.box_log2 = 0;
+  while ((1 << a.box_log2) < box) ++a.box_log2;
+  return p.kv_dtype == SKV_I8 ? launch_d<true>(m, a, num_ctas, p.head_dim, wide, tma, p.o_dtype, s)
+                              : launch_d<false>(m, a, num_ctas, p.head_dim, wide, tma, p.o_dtype, s);
 }
 
 }  // namespace skv

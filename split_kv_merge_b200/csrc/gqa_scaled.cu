@@ -3,7 +3,7 @@
 //   s_t = sm_scale (q . kcode_t) ks_t,   O = sum_t softmax(s)_t vs_t vcode_t,   LSE = ln sum_t e^{s_t}.
 // The scales leave both products: ks multiplies the finished scores, vs the softmax weights, so the
 // matrix instructions run on the codes themselves, which f16 holds exactly (e4m3: 4 significant
-// bits, 2^-9 .. 448; int8: integers).
+// bits, 2^-9 .. 448; int8: integers, carried as subnormals).
 //
 // Bound by HBM: 2 Hk D bytes per token.  One CTA takes `hc` KV heads (the largest of 8, 4, 2, 1 that
 // divides Hk) of a slice of the batch's tokens (persistent, slices cut equal by the planner), so a
@@ -110,6 +110,15 @@ __device__ __forceinline__ void cp_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// d = a . b + (c0, c0 in row g; c1, c1 in row g + 8)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                         float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %11, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -134,18 +143,19 @@ __device__ __forceinline__ float lds_f(uint32_t addr) {
   return v;
 }
 
-// four codes -> two f16 pairs, exact
+// Four codes -> two f16 pairs, exact.  An int8 code c becomes the subnormal f16 (c + 128) 2^-24 -- its
+// biased byte under a zero byte, one permute for two codes -- and the products start from minus 128
+// times the sum of the other operand (in 2^-24 units), which takes the bias out again.
+constexpr float kI8Unit = 1.f / 16777216.f;
 template <bool I8>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ uint32_t biased(uint32_t w) {
+  return I8 ? w ^ 0x80808080u : w;
+}
+template <bool I8>
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {  // w: biased
   if constexpr (I8) {
-    // bytes u = code + 128 under the exponent of 1024: the f16 1024 + u; minus 1152 is the code
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
+    lo = __byte_perm(w, 0u, 0x4140);
+    hi = __byte_perm(w, 0u, 0x4342);
   } else {
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
         : "=r"(lo), "=r"(hi)
@@ -161,6 +171,13 @@ __device__ __forceinline__ float ex2f(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// (o0, o1) += (c0, c1) f in one packed instruction
+__device__ __forceinline__ void fma_pair(float& o0, float& o1, float c0, float c1, float f) {
+  asm("{\n\t.reg .b64 o, c, f;\n\tmov.b64 o, {%0, %1};\n\tmov.b64 c, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\t"
+      "fma.rn.f32x2 o, c, f, o;\n\tmov.b64 {%0, %1}, o;\n\t}"
+      : "+f"(o0), "+f"(o1)
+      : "f"(c0), "f"(c1), "f"(f));
 }
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -372,6 +389,7 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
   constexpr int kKSteps = D / 16;      // k-steps of Q . K^T
   constexpr int kDims = D / 8;         // dims of O each lane column covers (n-tiles of P . V)
   constexpr int kRowSets = WIDE ? 2 : 1;
+  constexpr int kTokScales = TMA ? 1 : 2;  // scales of a lane's two tokens of an 8-token group
   // byte offset of the warp's 8-token groups in K (and V) of a stage, and of its scales
   uint32_t group_at[4];
 #pragma unroll
@@ -403,7 +421,7 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 
     // Q in f16 under the k permutation: k-step 4 j + s of chunk j holds dims 16 (4 j + t) + 4 s ..
     uint32_t qf[kKSteps][4];
-    float sc[2];
+    float sc[2], bias[2] = {0.f, 0.f};
     {
       float x[2][D / 4];
 #pragma unroll
@@ -428,9 +446,10 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         mx = quad_max(mx);
         const int e = mx > 0.f ? max((int)(__float_as_uint(mx) >> 23) - 127, -100) : 14;
         const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-        sc[s] = a.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+        sc[s] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - 14 + e) << 23) * (I8 ? 1.f / kI8Unit : 1.f);
+        const float by = a.scale_log2 < 0.f ? -up : up;  // factors of the scores stay >= 0
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) x[s][i] *= up;
+        for (int i = 0; i < D / 4; ++i) x[s][i] *= by;
       }
 #pragma unroll
       for (int ks = 0; ks < kKSteps; ++ks) {
@@ -439,6 +458,20 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         qf[ks][1] = WIDE ? pack_f16(x[1][i], x[1][i + 1]) : 0u;
         qf[ks][2] = pack_f16(x[0][i + 2], x[0][i + 3]);
         qf[ks][3] = WIDE ? pack_f16(x[1][i + 2], x[1][i + 3]) : 0u;
+      }
+      if constexpr (I8) {  // what the bias of K adds to a row's scores, of the values as rounded to f16
+#pragma unroll
+        for (int r = 0; r < kRowSets; ++r) {
+          float sum = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < kKSteps; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&qf[ks][2 * e + r]));
+              sum += y.x + y.y;
+            }
+          bias[r] = -128.f * kI8Unit * quad_sum(sum);
+        }
       }
     }
 
@@ -456,52 +489,61 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
       if (ok && tb < rg.t1) {
         const uint32_t kst = sbase + st * S::stage, vst = kst + S::kv;
         const uint32_t kss = sbase + st * S::stage + 2 * S::kv + scale_at, vss = kss + S::scales;
-        // ---- scores: 4 tiles of 8 tokens
+        // ---- scores: 4 tiles of 8 tokens, their accumulator chains interleaved
         float s[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t kw[4][4];
           const int tok = col_token<D>(g);
-          const uint32_t row = kst + group_at[n] + tok * D;
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 kw = lds128(row + (((4 * j + t) ^ swizzle<D>(tok)) << 4));
-            const uint32_t wd[4] = {kw.x, kw.y, kw.z, kw.w};
+          for (int n = 0; n < 4; ++n) {
+            const uint4 v = lds128(kst + group_at[n] + tok * D + (((4 * j + t) ^ swizzle<D>(tok)) << 4));
+            kw[n][0] = biased<I8>(v.x);
+            kw[n][1] = biased<I8>(v.y);
+            kw[n][2] = biased<I8>(v.z);
+            kw[n][3] = biased<I8>(v.w);
+          }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
               uint32_t b0, b1;
-              widen<I8>(wd[x], b0, b1);
-              mma16816(s[n], qf[4 * j + x], b0, b1);
+              widen<I8>(kw[n][x], b0, b1);
+              if (j == 0 && x == 0) mma16816(s[n], qf[0], b0, b1, bias[0], bias[1]);
+              else mma16816(s[n], qf[4 * j + x], b0, b1);
             }
-          }
         }
-        // ---- scale, mask, maximum
+        // ---- mask, maximum.  Scores stay unscaled: score = s * f, f = ks sc >= 0 (kept above 0, so that
+        // a masked -inf stays one; at 1e-30 every score of the block is 0 in any case)
         const int ta = col_token<D>(2 * t), tc1 = col_token<D>(2 * t + 1);
-        float vsc[4][2];
+        float vsc[4][kTokScales], f[kRowSets][4][kTokScales];
         float mx[2] = {-INFINITY, -INFINITY}, vref = 0.f;
-        const bool masked = tb + kWarpTokens > all_see;
+        if (tb + kWarpTokens > all_see) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          float k0, k1;
-          if constexpr (TMA) {  // one scale for the 8 tokens
-            k0 = k1 = lds_f(kss + 4 * n);
-            vsc[n][0] = vsc[n][1] = lds_f(vss + 4 * n);
-          } else {
-            k0 = lds_f(kss + (8 * n + ta) * 4);
-            k1 = lds_f(kss + (8 * n + tc1) * 4);
-            vsc[n][0] = lds_f(vss + (8 * n + ta) * 4);
-            vsc[n][1] = lds_f(vss + (8 * n + tc1) * 4);
-          }
-          vref = fmaxf(vref, fmaxf(vsc[n][0], vsc[n][1]));
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int r = 0; r < kRowSets; ++r) {
-            s[n][2 * r] *= k0 * sc[r];
-            s[n][2 * r + 1] *= k1 * sc[r];
-            if (masked) {
+            for (int r = 0; r < kRowSets; ++r) {
               if (tb + 8 * n + ta >= limit[r]) s[n][2 * r] = -INFINITY;
               if (tb + 8 * n + tc1 >= limit[r]) s[n][2 * r + 1] = -INFINITY;
             }
-            mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+          for (int e = 0; e < kTokScales; ++e) {  // TMA: one scale for the 8 tokens
+            const int at = TMA ? 4 * n : (8 * n + (e ? tc1 : ta)) * 4;
+            const float ks = lds_f(kss + at);
+            vsc[n][e] = lds_f(vss + at);
+            vref = fmaxf(vref, vsc[n][e]);
+#pragma unroll
+            for (int r = 0; r < kRowSets; ++r) f[r][n][e] = fmaxf(ks * sc[r], 1e-30f);
+          }
+#pragma unroll
+          for (int r = 0; r < kRowSets; ++r) {
+            if constexpr (kTokScales == 1)
+              mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]) * f[r][n][0]);
+            else
+              mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r] * f[r][n][0], s[n][2 * r + 1] * f[r][n][kTokScales - 1]));
           }
         }
         if constexpr (!TMA) vref = quad_max(vref);
@@ -529,20 +571,31 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // ---- weights
         uint32_t pf[2][4];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int n = 0; n < 4; ++n) {
+          const float v0 = vsc[n][0] * rv, v1 = kTokScales == 1 ? v0 : vsc[n][kTokScales - 1] * rv;
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int r = 0; r < 2; ++r) {
             if (r < kRowSets) {
-              const float mm = m[r] == -INFINITY ? 0.f : m[r];
-              const float p0 = ex2f(s[n][2 * r] - mm), p1 = ex2f(s[n][2 * r + 1] - mm);
+              const float nm = m[r] == -INFINITY ? 0.f : -m[r];
+              const float p0 = ex2f(fmaf(s[n][2 * r], f[r % kRowSets][n][0], nm));
+              const float p1 = ex2f(fmaf(s[n][2 * r + 1], f[r % kRowSets][n][kTokScales - 1], nm));
               l[r] += p0 + p1;
-              pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * (vsc[n][0] * rv), p1 * (vsc[n][1] * rv));
+              pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * v0, p1 * v1);
             } else {
               pf[n >> 1][(n & 1) * 2 + r] = 0u;
             }
           }
         }
         // ---- O += P . V: per lane 16 (D = 128) or 8 dims of 8 tokens
+        float unbias[2] = {0.f, 0.f};
+        if constexpr (I8) {  // the sum of the rounded weights: a product with f16 ones
+          float w1[4];
+          mma16816(w1, pf[0], 0x3C003C00u, 0x3C003C00u, 0.f, 0.f);
+          mma16816(w1, pf[1], 0x3C003C00u, 0x3C003C00u);
+          unbias[0] = -128.f * kI8Unit * w1[0];
+          unbias[1] = -128.f * kI8Unit * w1[2];
+        }
+        const float vmul = I8 ? vref * (1.f / kI8Unit) : vref;
         constexpr int kWords = D / 32;  // words of a lane's run of dims
         uint32_t vw[4][2][kWords];      // [8-token group][token of the pair][word]
 #pragma unroll
@@ -553,17 +606,17 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const uint32_t row = vst + group_at[n] + tok * D;
             if constexpr (D == 128) {
               const uint4 v = lds128(row + ((col_token<D>(g) ^ swizzle<D>(tok)) << 4));
-              vw[n][e][0] = v.x;
-              vw[n][e][1] = v.y;
-              vw[n][e][2] = v.z;
-              vw[n][e][3] = v.w;
+              vw[n][e][0] = biased<I8>(v.x);
+              vw[n][e][1] = biased<I8>(v.y);
+              vw[n][e][2] = biased<I8>(v.z);
+              vw[n][e][3] = biased<I8>(v.w);
             } else {
               const uint2 v = lds64(row + (((g >> 1) ^ swizzle<D>(tok)) << 4) + ((g & 1) << 3));
-              vw[n][e][0] = v.x;
-              vw[n][e][1] = v.y;
+              vw[n][e][0] = biased<I8>(v.x);
+              vw[n][e][1] = biased<I8>(v.y);
             }
           }
-        if (TMA && tb + kWarpTokens > rg.t1) {  // slots past the end hold anything: 0 x NaN is not 0
+        if (TMA && !I8 && tb + kWarpTokens > rg.t1) {  // slots past the end may hold NaN, and 0 x NaN is not 0
 #pragma unroll
           for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -580,14 +633,16 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             widen<I8>(__byte_perm(vw[n][0][q], vw[n][1][q], 0x5140), b[n][0], b[n][1]);
             widen<I8>(__byte_perm(vw[n][0][q], vw[n][1][q], 0x7362), b[n][2], b[n][3]);
           }
+          float c[4][4];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(c, pf[0], b[0][d], b[1][d]);
-            mma16816(c, pf[1], b[2][d], b[3][d]);
+          for (int d = 0; d < 4; ++d) mma16816(c[d], pf[0], b[0][d], b[1][d], unbias[0], unbias[1]);
 #pragma unroll
-            for (int x = 0; x < 2 * kRowSets; ++x) o[4 * q + d][x] = fmaf(c[x], vref, o[4 * q + d][x]);
-          }
+          for (int d = 0; d < 4; ++d) mma16816(c[d], pf[1], b[2][d], b[3][d]);
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+#pragma unroll
+            for (int r = 0; r < kRowSets; ++r)
+              fma_pair(o[4 * q + d][2 * r], o[4 * q + d][2 * r + 1], c[d][2 * r], c[d][2 * r + 1], vmul);
         }
       }
       __syncwarp();

@@ -155,6 +155,26 @@ def test_rising_scores_and_extreme_scales(cache):
     _check(c, o, lse, False)
 
 
+@pytest.mark.parametrize("cache,block", [("e4m3", 16), ("i8", 16), ("i8", 4)])
+def test_negative_softmax_scale_and_large_queries(cache, block):
+    c = Case(15, [70, 300], [2, 1], 16, 2, 128, 16, block, cache)
+    c.q *= 512.0
+    o, lse, _ = _run(c, True, sm_scale=-0.0003)
+    _check_scaled(c, o, lse, -0.0003)
+
+
+def _check_scaled(c, o, lse, sm_scale):
+    """As _check, with the score magnitudes taken at |sm_scale|."""
+    q = c.q.double().cpu().numpy()
+    args = (lambda r: c.values(0, r), lambda r: c.values(1, r), c.qo_indptr, c.lengths, c.hk, True)
+    O, LSE, A, _ = OS.packed_attention(q, *args, sm_scale)
+    M = OS.packed_attention(np.abs(q), lambda r: np.abs(c.values(0, r)), args[1], *args[2:], abs(sm_scale))[3]
+    e = (c.d + 4) * 2.0 ** -23 * M + 2.0 ** -22 + 300 * 2.0 ** -24
+    assert np.all(np.abs(lse.cpu().numpy() - LSE) <= e + 2.0 ** -23 * np.abs(LSE))
+    vmax = max(np.abs(c.values(1, r)).max() for r in range(2))
+    assert np.all(np.abs(o.cpu().numpy() - O) <= A * (2.0 ** -10 + 2 * e[..., None]) + 300 * 2.0 ** -25 * vmax)
+
+
 def test_zero_scales_everywhere():
     c = Case(6, [40, 3], [1, 1], 8, 2, 64, 16, 16, "i8", poison=False)
     c.scale[0][:], c.scale[1][:] = 0.0, 0.0

@@ -10,16 +10,21 @@
 // tokens (they share every K and V tile), or, for odd groups, consecutive 128-token tiles of a head.
 //
 // TMEM holds S_A, S_B (128 fp32 columns each) and O_A, O_B; P (bf16) overwrites the first half of its
-// own S and is the A operand of P V straight from TMEM.  MMAs of one CTA are issued by one thread
-// and complete in order, so two facts need no barrier of their own: Q K^T of the next tile may
-// overwrite S / P as soon as it is issued after P V, and a full S means the P V before it is done,
-// so the softmax warps may rescale O.  The running maximum is raised only when a score passes it
-// by 2^8, so after the first tiles O is rarely rescaled.
+// own S and is the A operand of P V straight from TMEM.  The MMAs of a query tile are issued by one
+// thread and complete in order, so two facts need no barrier of their own: Q K^T of the next tile
+// may overwrite S / P as soon as it is issued after P V, and a full S means the P V before it is
+// done, so the softmax warps may rescale O.  A and B have an issuing warp each: an MMA of these
+// shapes holds its issuer about 80 cycles (it runs for 64), a wait or commit after one some 200, and
+// one issuer for both sides was busy 4130 cycles per pair of tiles (clock stamps of one CTA).  The two
+// issue in strict turns: left to themselves A and B fall into step, both in the softmax and then both
+// at the tensor cores (1214 us against TURNS us on 4096 query tokens over 16384 keys, 32/8 heads).
+// The running maximum is raised only when a score passes it by 2^8, so O is rarely rescaled.
 //
 // Persistent: the planner hands every CTA a list of items (a pair of query tiles and a range of
 // key tiles), longest first onto the least loaded.  Items of few rows over many keys are cut along
 // the keys into fp32 partials that the merge pass joins.  Roles: warps 0-3 softmax of A, 4-7 of B,
-// warp 8 TMA (ring of K and V tiles in the order of use), warp 9 MMA.  All waits are bounded.
+// warp 8 TMA (ring of K and V tiles in the order of use), warps 9 and 10 the MMAs of A and of B.
+// All waits are bounded.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -33,7 +38,7 @@ namespace skv {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreads = 384;         // three warpgroups; the last one's warps 2 and 3 idle
+constexpr int kThreads = 384;         // three warpgroups; the last one's warp 3 idles
 // Registers: 384 threads start with 168; the softmax warpgroups hold a whole row of scores, so they
 // take 208 and the third gives up to 88 (2 x 128 x 208 + 128 x 88 = 384 x 168).
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
@@ -48,7 +53,7 @@ struct Smem {
   static constexpr int q = 0;                       // Q_A, Q_B
   static constexpr int kv = 2 * tile;
   static constexpr int bars = kv + slots * tile;
-  static constexpr int nbars = 2 * slots + 2 + 6;
+  static constexpr int nbars = 2 * slots + 2 + 8;
   static constexpr int misc = bars + nbars * 8;
   static constexpr int total = misc + 16;
 };
@@ -104,6 +109,29 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// One row of a tile: p = 2^(s * scale - m), bf16 pairs into the row's P columns, their sum into la.
+// (Two to four of every eight pairs by a polynomial on the FMA pipe measured slower: 1038 and 1118 us
+// against 1011; the warps are bound by instructions, not by the exponential unit.)
+__device__ __forceinline__ void weights(const float (&s)[kTile], uint64_t sc2, uint64_t nm2, uint32_t ts,
+                                        uint64_t (&la)[2]) {
+#pragma unroll
+  for (int c = 0; c < kTile; c += 32) {
+    float pw[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t x2 = fma2(pk2(s[c + e], s[c + e + 1]), sc2, nm2);
+      float p0, p1;
+      upk2(x2, p0, p1);
+      p0 = ex2(p0);
+      p1 = ex2(p1);
+      const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+      pw[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+      la[(e >> 1) & 1] = add2(la[(e >> 1) & 1], pk2(p0, p1));
+    }
+    tc::tmem_st_x16(ts + c / 2, pw);
+  }
+}
+
 // The two query tiles of an item, and the key tiles [0, tiles) of its range that each one needs.
 struct Side {
   int q0, n, head, limit, tiles;
@@ -140,18 +168,20 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   auto sfull_bar = [&](int x) { return qempty + 8u + 8u * x; };
   auto pfull_bar = [&](int x) { return qempty + 24u + 8u * x; };
   auto ofull_bar = [&](int x) { return qempty + 40u + 8u * x; };
+  auto turn_bar = [&](int x) { return qempty + 56u + 8u * x; };
 
   if (tid == 0) {
     for (int s = 0; s < S::slots; ++s) {
       tc::mbar_init(full_bar(s), 1);
-      tc::mbar_init(empty_bar(s), 1);
+      tc::mbar_init(empty_bar(s), 2);  // both sides
     }
     tc::mbar_init(qfull, 1);
-    tc::mbar_init(qempty, 1);
+    tc::mbar_init(qempty, 2);
     for (int x = 0; x < 2; ++x) {
       tc::mbar_init(sfull_bar(x), 1);
       tc::mbar_init(pfull_bar(x), 4);
       tc::mbar_init(ofull_bar(x), 1);
+      tc::mbar_init(turn_bar(x), 1);
     }
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -206,9 +236,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         ++q_it;
         const int kh = w.ha / a.group, row0 = w.kv0 + w.tile_begin * kTile;
         load_kv(&kmap, kh, row0);
-        for (int j = 0; j < tiles && ok; ++j) {  // in the order of use: K(j + 1), V(j)
-          if (j + 1 < tiles) load_kv(&kmap, kh, row0 + (j + 1) * kTile);
-          if (ok) load_kv(&vmap, kh, row0 + j * kTile);
+        for (int j = 0; j < tiles && ok; ++j) {  // in the order of use
+          load_kv(&vmap, kh, row0 + j * kTile);
+          if (ok && j + 1 < tiles) load_kv(&kmap, kh, row0 + (j + 1) * kTile);
         }
       }
       if (!ok && lane == 0) {  // copies in flight may still be landing: wait for them (bounded)
@@ -220,69 +250,78 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         for (int t = max(0, slot_it - S::slots); t < slot_it; ++t) drain(full_bar(t % S::slots), (t / S::slots) & 1);
         if (q_it > 0) drain(qfull, (q_it - 1) & 1);
       }
-    } else if (warp == 9) {
-      // ==================================================================================== MMA
+    } else if (warp < 11) {
+      // =================================================================== MMA of one query tile
       if (lane == 0) {
         constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, kTile, false, false);
         constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, false, true);
-        int slot_it = 0, q_it = 0, p_it[2] = {0, 0};
+        const int x = warp - 9;
+        const uint32_t qs = sbase + S::q + x * S::tile, ts = tm_s[x], to = tm_o[x];
+        int slot_it = 0, q_it = 0, p_it = 0, turn = 0;
         bool ok = true;
+        // A and B issue in turns, one group (P V, then the next Q K^T) each
+        auto take_turn = [&]() {
+          if (x == 1) ok = tc::mbar_wait(turn_bar(1), turn & 1, abort_flag, a.status) && ok;
+          else if (turn > 0) ok = tc::mbar_wait(turn_bar(0), (turn - 1) & 1, abort_flag, a.status) && ok;
+          ++turn;
+        };
+        auto pass_turn = [&]() { tc::mbar_arrive(turn_bar(1 - x)); };
         auto wait_slot = [&]() {
           const int st = slot_it % S::slots;
-          ok = tc::mbar_wait(full_bar(st), (slot_it / S::slots) & 1, abort_flag, a.status);
-          tc::tc_fence_after();
+          ok = tc::mbar_wait(full_bar(st), (slot_it / S::slots) & 1, abort_flag, a.status) && ok;
           ++slot_it;
           return st;
         };
-        auto qk = [&](int x, int st) {
-          const uint32_t qs = sbase + S::q + x * S::tile, ks = sbase + S::kv + st * S::tile;
-  #pragma unroll
+        // a tile or Q handed back: when the MMAs that read it are done, or at once where none did
+        auto release = [&](uint32_t bar, bool used) {
+          if (used) tc::mma_commit(bar);
+          else tc::mbar_arrive(bar);
+        };
+        auto qk = [&](int st) {
+          const uint32_t ks = sbase + S::kv + st * S::tile;
+          tc::tc_fence_after();
+#pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16(tm_s[x], tc::sdesc_sw128(qs + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024),
+            tc::mma_bf16(ts, tc::sdesc_sw128(qs + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024),
                          tc::sdesc_sw128(ks + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
           tc::mma_commit(sfull_bar(x));
         };
         for (int i = i_begin; i < i_end && ok; ++i) {
           const PromptItem w = a.items[i];
-          const Side s[2] = {side_of(w, 0), side_of(w, 1)};
-          const int tiles = max(s[0].tiles, s[1].tiles);
-          if (tiles == 0) continue;
+          const int tiles = side_of(w, x).tiles, all = max(tiles, side_of(w, 1 - x).tiles);
+          if (all == 0) continue;
           ok = tc::mbar_wait(qfull, q_it & 1, abort_flag, a.status);
           ++q_it;
-          if (!ok) break;
           int kst = wait_slot();
+          take_turn();
           if (!ok) break;
-  #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            if (s[x].tiles > 0) qk(x, kst);
-          tc::mma_commit(empty_bar(kst));
-          if (tiles == 1) tc::mma_commit(qempty);
-          for (int j = 0; j < tiles && ok; ++j) {
-            const bool more = j + 1 < tiles;
-            if (more) kst = wait_slot();
-            if (!ok) break;
+          if (tiles > 0) qk(kst);
+          pass_turn();
+          release(empty_bar(kst), tiles > 0);
+          if (tiles <= 1) release(qempty, tiles > 0);
+          for (int j = 0; j < all; ++j) {
             const int vst = wait_slot();
-            if (!ok) break;
-            const uint32_t vs = sbase + S::kv + vst * S::tile;
-  #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (j < s[x].tiles) {
-                ok = tc::mbar_wait(pfull_bar(x), p_it[x] & 1, abort_flag, a.status);
-                ++p_it[x];
-                if (!ok) break;
-                tc::tc_fence_after();
-  #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 packed columns of P
-                  mma_ts(tm_o[x], tm_s[x] + k * 8, tc::sdesc_sw128(vs + k * 2048, kRegion, 1024), idesc_o,
-                         (j > 0 || k > 0) ? 1u : 0u);
-                if (j + 1 == s[x].tiles) tc::mma_commit(ofull_bar(x));
-              }
-              if (j + 1 < s[x].tiles) qk(x, kst);
+            if (j + 1 < all) kst = wait_slot();
+            if (j < tiles) {
+              ok = tc::mbar_wait(pfull_bar(x), p_it & 1, abort_flag, a.status) && ok;
+              ++p_it;
             }
+            take_turn();
             if (!ok) break;
-            if (more) tc::mma_commit(empty_bar(kst));
+            if (j < tiles) {
+              tc::tc_fence_after();
+              const uint32_t vs = sbase + S::kv + vst * S::tile;
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 packed columns of P
+                mma_ts(to, ts + k * 8, tc::sdesc_sw128(vs + k * 2048, kRegion, 1024), idesc_o,
+                       (j > 0 || k > 0) ? 1u : 0u);
+              if (j + 1 == tiles) tc::mma_commit(ofull_bar(x));
+            }
+            if (j + 1 < tiles) qk(kst);
+            pass_turn();
+            release(empty_bar(vst), j < tiles);
+            if (j + 1 < all) release(empty_bar(kst), j + 1 < tiles);
             if (j + 2 == tiles) tc::mma_commit(qempty);
-            tc::mma_commit(empty_bar(vst));
           }
         }
       }
@@ -299,11 +338,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     bool ok = true;
     for (int i = i_begin; i < i_end; ++i) {
       const PromptItem w = a.items[i];
-      const Side s_me = side_of(w, x), s_other = side_of(w, 1 - x);
-      const int tiles = s_me.tiles, all_tiles = max(tiles, s_other.tiles);
-      // l: sum of the exact weights (for the LSE); lr: of the rounded ones that P V multiplies (the
-      // divisor of O, so that a row with one dominant key returns that key's V)
-      float m = -INFINITY, l = 0.f, lr = 0.f;
+      const Side s_me = side_of(w, x);
+      const int tiles = s_me.tiles, all_tiles = max(tiles, side_of(w, 1 - x).tiles);
+      // l: sum of the exact weights, the divisor of O too: P V multiplies them rounded to bf16, each
+      // off by 2^-9 at most and to either side, as far as a bf16 O is from its own value
+      float m = -INFINITY, l = 0.f;
       const int64_t lim64 = w.causal ? min((int64_t)w.kv_len, (int64_t)s_me.limit + r) : (int64_t)w.kv_len;
       const int limit = (int)max(lim64, (int64_t)0);
       const int warp_limit = __shfl_sync(0xffffffffu, limit, 0);  // the warp's first row sees fewest
@@ -343,7 +382,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           const float mn = raise ? mx : m;
           const float al = mn == m ? 1.f : ex2(m - mn);
           l *= al;
-          lr *= al;
           m = mn;
           if (j > 0) {  // a full S(j) means P V(j - 1) is done
 #pragma unroll
@@ -357,10 +395,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
             }
           }
         }
-        if (key0 + kTile > w.kv_len && (x == 0 || j >= s_other.tiles)) {
-          // keys past the sequence belong to another one (or to nobody): their V rows become zero,
-          // by A's warps, or by B's where A has no such tile
-          const int seq = v_seq + (j + 1 < all_tiles ? 2 * j + 2 : 2 * j + 1);  // ring position of V(j)
+        if (key0 + kTile > w.kv_len) {
+          // keys past the sequence belong to another one (or to nobody): their V rows become zero
+          // before either side multiplies them (both sides may write the same zeros)
+          const int seq = v_seq + 2 * j + 1;  // ring position of V(j)
           const int st = seq % S::slots;
           ok = tc::mbar_wait(full_bar(st), (seq / S::slots) & 1, abort_flag, a.status) && ok;
           uint8_t* vb = smem + S::kv + st * S::tile;
@@ -375,29 +413,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         }
         const float mm = m == -INFINITY ? 0.f : m;
         const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-mm, -mm);
-        uint64_t la[2] = {0, 0}, lb[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float pw[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x0, x1;
-            upk2(fma2(pk2(s[c + e], s[c + e + 1]), sc2, nm2), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(&h2);
-            pw[e >> 1] = __uint_as_float(u);
-            la[(e >> 1) & 1] = add2(la[(e >> 1) & 1], pk2(p0, p1));
-            lb[(e >> 1) & 1] = add2(lb[(e >> 1) & 1], pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)));
-          }
-          tc::tmem_st_x16(ts + c / 2, pw);
-        }
+        uint64_t la[2] = {0, 0};
+        weights(s, sc2, nm2, ts, la);
         {
-          float a0, a1, b0, b1;
+          float a0, a1;
           upk2(add2(la[0], la[1]), a0, a1);
-          upk2(add2(lb[0], lb[1]), b0, b1);
           l += a0 + a1;
-          lr += b0 + b1;
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -412,7 +433,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
       const bool live = r < s_me.n && s_me.q0 + r < a.total_q;
       const bool some = l > 0.f || l != l;
-      const float inv = some ? 1.f / lr : 0.f;
+      const float inv = some ? 1.f / l : 0.f;
       OutT* oo = nullptr;
       float* op = nullptr;
       if (live) {

@@ -252,64 +252,71 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
     } else if (warp < 11) {
       // =================================================================== MMA of one query tile
-      if (lane == 0) {
-        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, kTile, false, false);
-        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, false, true);
-        const int x = warp - 9;
-        const uint32_t qs = sbase + S::q + x * S::tile, ts = tm_s[x], to = tm_o[x];
-        int slot_it = 0, q_it = 0, p_it = 0, turn = 0;
-        bool ok = true;
-        // A and B issue in turns, one group (P V, then the next Q K^T) each
-        auto take_turn = [&]() {
-          if (x == 1) ok = tc::mbar_wait(turn_bar(1), turn & 1, abort_flag, a.status) && ok;
-          else if (turn > 0) ok = tc::mbar_wait(turn_bar(0), (turn - 1) & 1, abort_flag, a.status) && ok;
-          ++turn;
-        };
-        auto pass_turn = [&]() { tc::mbar_arrive(turn_bar(1 - x)); };
-        auto wait_slot = [&]() {
-          const int st = slot_it % S::slots;
-          ok = tc::mbar_wait(full_bar(st), (slot_it / S::slots) & 1, abort_flag, a.status) && ok;
-          ++slot_it;
-          return st;
-        };
-        // a tile or Q handed back: when the MMAs that read it are done, or at once where none did
-        auto release = [&](uint32_t bar, bool used) {
-          if (used) tc::mma_commit(bar);
-          else tc::mbar_arrive(bar);
-        };
-        auto qk = [&](int st) {
-          const uint32_t ks = sbase + S::kv + st * S::tile;
-          tc::tc_fence_after();
+      // The whole warp keeps the loop and the waits; lane 0 issues.  (A lane that waits alone, with the
+      // others parked at the end of the kernel, wakes late: 976 us against 957 with whole-warp waits.)
+      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, kTile, false, false);
+      constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, false, true);
+      const int x = warp - 9;
+      const uint32_t qs = sbase + S::q + x * S::tile, ts = tm_s[x], to = tm_o[x];
+      int slot_it = 0, q_it = 0, p_it = 0, turn = 0;
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, a.status)) && ok;
+      };
+      // A and B issue in turns, one group (P V, then the next Q K^T) each
+      auto take_turn = [&]() {
+        if (x == 1) wait(turn_bar(1), turn & 1);
+        else if (turn > 0) wait(turn_bar(0), (turn - 1) & 1);
+        ++turn;
+      };
+      auto wait_slot = [&]() {
+        const int st = slot_it % S::slots;
+        wait(full_bar(st), (slot_it / S::slots) & 1);
+        ++slot_it;
+        return st;
+      };
+      // a tile or Q handed back: when the MMAs that read it are done, or at once where none did
+      auto release = [&](uint32_t bar, bool used) {
+        if (used) tc::mma_commit(bar);
+        else tc::mbar_arrive(bar);
+      };
+      auto qk = [&](int st) {
+        const uint32_t ks = sbase + S::kv + st * S::tile;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16(ts, tc::sdesc_sw128(qs + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024),
-                         tc::sdesc_sw128(ks + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
-          tc::mma_commit(sfull_bar(x));
-        };
-        for (int i = i_begin; i < i_end && ok; ++i) {
-          const PromptItem w = a.items[i];
-          const int tiles = side_of(w, x).tiles, all = max(tiles, side_of(w, 1 - x).tiles);
-          if (all == 0) continue;
-          ok = tc::mbar_wait(qfull, q_it & 1, abort_flag, a.status);
-          ++q_it;
-          int kst = wait_slot();
-          take_turn();
-          if (!ok) break;
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_bf16(ts, tc::sdesc_sw128(qs + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024),
+                       tc::sdesc_sw128(ks + (k >> 2) * kRegion + (k & 3) * 32, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
+        tc::mma_commit(sfull_bar(x));
+      };
+      for (int i = i_begin; i < i_end && ok; ++i) {
+        const PromptItem w = a.items[i];
+        const int tiles = side_of(w, x).tiles, all = max(tiles, side_of(w, 1 - x).tiles);
+        if (all == 0) continue;
+        wait(qfull, q_it & 1);
+        ++q_it;
+        int kst = wait_slot();
+        take_turn();
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (lane == 0) {
           if (tiles > 0) qk(kst);
-          pass_turn();
+          tc::mbar_arrive(turn_bar(1 - x));
           release(empty_bar(kst), tiles > 0);
           if (tiles <= 1) release(qempty, tiles > 0);
-          for (int j = 0; j < all; ++j) {
-            const int vst = wait_slot();
-            if (j + 1 < all) kst = wait_slot();
+        }
+        __syncwarp();
+        for (int j = 0; j < all; ++j) {
+          const int vst = wait_slot();
+          if (j + 1 < all) kst = wait_slot();
+          take_turn();  // free long before P is: one wait less behind P
+          if (j < tiles) {
+            wait(pfull_bar(x), p_it & 1);
+            ++p_it;
+          }
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lane == 0) {
             if (j < tiles) {
-              ok = tc::mbar_wait(pfull_bar(x), p_it & 1, abort_flag, a.status) && ok;
-              ++p_it;
-            }
-            take_turn();
-            if (!ok) break;
-            if (j < tiles) {
-              tc::tc_fence_after();
               const uint32_t vs = sbase + S::kv + vst * S::tile;
 #pragma unroll
               for (int k = 0; k < kTile / 16; ++k)  // 16 keys: 8 packed columns of P
@@ -318,11 +325,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
               if (j + 1 == tiles) tc::mma_commit(ofull_bar(x));
             }
             if (j + 1 < tiles) qk(kst);
-            pass_turn();
+            tc::mbar_arrive(turn_bar(1 - x));
             release(empty_bar(vst), j < tiles);
             if (j + 1 < all) release(empty_bar(kst), j + 1 < tiles);
             if (j + 2 == tiles) tc::mma_commit(qempty);
           }
+          __syncwarp();
         }
       }
     }

@@ -10,12 +10,15 @@
 // its threads, one 16-value item of a row each.
 //
 // Block-scaled caches (append_blocks_kernel): the unit is a segment -- the new tokens of one
-// request that fall into one scale block -- for four heads of K or of V: a warp owns a head, takes
-// the maximum of its (rotated) rows, settles the scale, re-encodes the block's other codes if the
-// scale grew, then encodes the new rows.  Segments of up to 4 rows per lane stay in registers
-// between the two passes; longer ones are read again from L1 / L2.  One owner per (block, head):
-// no atomics, results do not depend on order.  Window w of the grid takes the segments that begin
-// among its rows; the last blocks of the grid rotate Q.
+// request that fall into one scale block -- of K or of V.  A block of sixteen warps forms the segment's
+// (cos, sin) table once and goes through the heads, as many at a time as the segment's length leaves
+// warps for (one warp a head for a few tokens, all sixteen for 64): take the maximum of the head's
+// (rotated) rows, settle the scale, re-encode the block's other codes if the scale grew, encode the
+// rows from registers while the next heads' rows are on their way.  Segments of more than 64 tokens
+// are read twice.  One owner per (block, head): no atomics, results do not depend on order.  Window w
+// of the grid takes the segments that begin among its rows; the last blocks of the grid rotate Q.
+// (One warp per head, two passes over its rows: 93 us for 20 k tokens in blocks of 64; eight warps for
+// two heads, each with its own search and table: 121 us; this form: SEGMENT_US us.)
 #include "rope.cuh"
 
 #include <cuda_fp8.h>
@@ -29,11 +32,11 @@ namespace {
 using rope::Freq;
 
 constexpr int kRowThreads = 256;
-constexpr int kBlockThreads = 128;
+constexpr int kBlockWarps = 16;  // block kernel
 constexpr int kMaxTokens = 16;   // tokens per block of threads, row kernel
 constexpr int kTableTokens = 64; // tokens whose tables are held at once, block kernel
-constexpr int kKeep = 4;         // items each lane holds between the two passes
 
+enum Turn { kCopy = 0, kInterleaved = 1, kHalves = 2 };
 enum CacheMode { MODE_BF16 = 0, MODE_E4M3 = 1, MODE_NONE = 2 };
 
 struct AppendArgs {
@@ -56,7 +59,8 @@ struct AppendArgs {
   int32_t* status;
   int batch, num_rows, num_pages, page_size, hk, hq, head_dim, block_tokens;
   int per_block;        // rows of a window
-  int num_windows, num_head_groups, num_kv_blocks;
+  int per_q_block;      // rows of a block of threads that rotates Q beside the block kernel
+  int num_windows;
   float inv_scale;
   Freq f;
 };
@@ -74,8 +78,8 @@ __device__ __forceinline__ int find_request(const int32_t* ip, int batch, int t,
   return lo;
 }
 
-// Where row t goes (warp-collective).  ok: the row belongs to a request of a sound table; page < 0:
-// its page id is out of range.
+// Where row t goes (warp-collective).  ok: the row belongs to a request of a sound table.  The page
+// id is as the table has it (checked by sound_page, so that its load can be in flight meanwhile).
 struct Place {
   int r, i, n, pos, page;
   bool ok;
@@ -88,18 +92,17 @@ __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, int lane
   pl.n = __ldg(a.ip + pl.r + 1) - row0;
   const int p0 = __ldg(a.kv_indptr + pl.r), np = __ldg(a.kv_indptr + pl.r + 1) - p0;
   const int64_t len = np > 0 ? (int64_t)(np - 1) * a.page_size + __ldg(a.last + pl.r) : 0;
-  const int64_t pos = len - pl.n + pl.i;
-  pl.pos = (int)pos;
   pl.page = -1;
-  pl.ok = pl.i >= 0 && pl.i < pl.n && len >= pl.n && pos / a.page_size < np;
-  if (pl.ok) {
-    const int page = __ldg(a.kv_indices + (int64_t)p0 + pl.pos / a.page_size);
-    if ((unsigned)page < (unsigned)a.num_pages) pl.page = page;
-    else if (lane == 0) report(a.status, SKV_DEV_PAGE_OOB);
-  } else if (lane == 0) {
-    report(a.status, SKV_DEV_PLAN_BAD);
-  }
+  pl.ok = pl.i >= 0 && pl.i < pl.n && len >= pl.n && len <= (int64_t)np * a.page_size && len <= INT32_MAX;
+  pl.pos = pl.ok ? (int)len - pl.n + pl.i : 0;
+  if (pl.ok) pl.page = __ldg(a.kv_indices + (int64_t)p0 + pl.pos / a.page_size);
+  else if (lane == 0) report(a.status, SKV_DEV_PLAN_BAD);
   return pl;
+}
+__device__ __forceinline__ bool sound_page(const AppendArgs& a, int page, int lane) {
+  if ((unsigned)page < (unsigned)a.num_pages) return true;
+  if (lane == 0) report(a.status, SKV_DEV_PAGE_OOB);
+  return false;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -118,14 +121,13 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
 }
 // An item's 16 codes: 8 bytes for each chunk.
 template <bool I8>
-__device__ __forceinline__ void store_codes(uint8_t* row, const rope::Item& it, const float (&x)[16], float inv) {
-  float y[16];
+__device__ __forceinline__ void encode_item(const float (&x)[16], float inv, uint2 (&code)[2]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) y[j] = x[j] * inv;
-  *reinterpret_cast<uint2*>(row + it.c0) =
-      make_uint2(codes4<I8>(y[0], y[1], y[2], y[3]), codes4<I8>(y[4], y[5], y[6], y[7]));
-  *reinterpret_cast<uint2*>(row + it.c1) =
-      make_uint2(codes4<I8>(y[8], y[9], y[10], y[11]), codes4<I8>(y[12], y[13], y[14], y[15]));
+  for (int c = 0; c < 2; ++c) {
+    const float* y = x + 8 * c;
+    code[c] = make_uint2(codes4<I8>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                         codes4<I8>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+  }
 }
 
 // Block-wide: rows [t0, t0 + n) of K and V into a cache without block scales (MODE_NONE: neither)
@@ -154,7 +156,7 @@ __device__ __forceinline__ void rows_pass(const AppendArgs& a, int t0, int n, fl
     const Place pl = find_place(a, t0 + j, lane);
     if (lane == 0) {
       s_pos[j] = a.positions != nullptr ? __ldg(a.positions + t0 + j) : pl.pos;
-      s_page[j] = pl.page;
+      s_page[j] = MODE != MODE_NONE && pl.ok && sound_page(a, pl.page, 0) ? pl.page : -1;
       s_slot[j] = pl.pos % a.page_size;
       s_ok[j] = pl.ok;
     }
@@ -182,7 +184,12 @@ __device__ __forceinline__ void rows_pass(const AppendArgs& a, int t0, int n, fl
                                : (int64_t)s_page[tk] * a.kc0 + (int64_t)s_slot[tk] * a.kc1 + (int64_t)hd * a.kc2;
       uint8_t* base = is_v ? a.vc : a.kc;
       if constexpr (MODE == MODE_BF16) rope::store_item(reinterpret_cast<__nv_bfloat16*>(base) + off, it, x);
-      else store_codes<false>(base + off, it, x, a.inv_scale);
+      else {
+        uint2 code[2];
+        encode_item<false>(x, a.inv_scale, code);
+        *reinterpret_cast<uint2*>(base + off + it.c0) = code[0];
+        *reinterpret_cast<uint2*>(base + off + it.c1) = code[1];
+      }
     }
   }
 }
@@ -194,103 +201,153 @@ __global__ void __launch_bounds__(kRowThreads) append_rows_kernel(const __grid_c
   rows_pass<MODE, kRowThreads>(a, t0, min(a.per_block, a.num_rows - t0), table);
 }
 
-// One segment of one head, by one warp: rows [t0, t0 + cnt) of `src` into slots [slot0, ...) of the
-// block whose first slot is slot0 - old.  Block-wide barriers when TURN (table refills), so every
-// warp of the block calls it; `live` is false for warps without a head.
-template <bool I8, bool TURN>
-__device__ __forceinline__ void segment(const AppendArgs& a, const __nv_bfloat16* src, int64_t s0, uint8_t* dst,
-                                        int64_t d1, float* scale, int t0, int cnt, int old, int pos, bool live,
-                                        float4* table, int32_t* s_pos) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int items = a.head_dim / 16, item = lane % items, lt = 32 / items, sub = lane / items;
-  const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
-  const rope::Item it = rope::item_of(item, a.f.dim, a.f.halves, a.head_dim);
-  rope::Raw<__nv_bfloat16> raw[kKeep];
-  const int step = lt * kKeep;  // tokens the warp holds at once
-  const bool once = cnt <= step;
-  float amax = 0.f, inv = 0.f;
-  auto load = [&](int base, int end) {
+// Shared memory of the block kernel beside the table.
+struct BlockShared {
+  int32_t pos[kTableTokens];
+  uint32_t amax[2][kBlockWarps];
+};
+
+// K's or V's pointers (V is a constant of the caller: strides stay in the parameter bank).
+template <bool V>
+__device__ __forceinline__ const __nv_bfloat16* row_ptr(const AppendArgs& a, int t, int h) {
+  return V ? a.v + t * a.v0 + h * a.v1 : a.k + t * a.k0 + h * a.k1;
+}
+template <bool V>
+__device__ __forceinline__ uint8_t* cache_ptr(const AppendArgs& a, int page, int slot, int h) {
+  return V ? a.vc + page * a.vc0 + slot * a.vc1 + h * a.vc2 : a.kc + page * a.kc0 + slot * a.kc1 + h * a.kc2;
+}
+template <bool V>
+__device__ __forceinline__ float* scale_ptr(const AppendArgs& a, int page, int blk, int h) {
+  return V ? a.vsc + page * a.vs0 + blk * a.vs1 + h * a.vs2 : a.ksc + page * a.ks0 + blk * a.ks1 + h * a.ks2;
+}
+
+// The codes of a block's slots outside [old, old + cnt), written again for a scale 1 / inv.
+template <bool I8>
+__device__ __noinline__ void reencode(uint8_t* dst, int64_t row, int tokens, int old, int cnt, int sub, int lanes, int item,
+                                      float before, float inv) {
+  for (int j = sub; j < tokens; j += lanes) {
+    if (j >= old && j < old + cnt) continue;
+    uint4* p = reinterpret_cast<uint4*>(dst + j * row + item * 16);
+    const uint4 w = *p;
+    uint32_t in[4] = {w.x, w.y, w.z, w.w}, out[4];
 #pragma unroll
-    for (int u = 0; u < kKeep; ++u) {
-      const int j = base + u * lt + sub;
-      if (live && j < end) raw[u].load(src + (int64_t)(t0 + j) * s0, it);
-    }
-  };
-  if (once) load(0, cnt);
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
-      const int cend = min(cnt, c0 + kTableTokens);
-      if (TURN && (pass == 0 || cnt > kTableTokens)) {
-        __syncthreads();  // the last table has been read
-        for (int j = tid; j < cend - c0; j += kBlockThreads)
-          s_pos[j] = a.positions != nullptr ? __ldg(a.positions + t0 + c0 + j) : pos + c0 + j;
-        __syncthreads();
-        rope::fill_table(table, s_pos, cend - c0, a.f, tid, kBlockThreads);
-        __syncthreads();
+    for (int e = 0; e < 4; ++e) {
+      float y[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t c = (in[e] >> (8 * b)) & 0xFFu;
+        y[b] = (I8 ? (float)(int8_t)c : e4m3_to_float(c)) * before * inv;
       }
-      for (int base = c0; base < cend; base += step) {
-        if (!once) load(base, cend);
-#pragma unroll
-        for (int u = 0; u < kKeep; ++u) {
-          const int j = base + u * lt + sub;
-          if (!live || j >= cend) continue;
-          float x[16];
-          raw[u].values(x);
-          if (TURN && it.turned) rope::turn_item(x, table + (j - c0) * stride4, item, nrot, a.f.halves);
-          if (pass == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-          } else {
-            store_codes<I8>(dst + (int64_t)(old + j) * d1, it, x, inv);
-          }
-        }
-      }
+      out[e] = codes4<I8>(y[0], y[1], y[2], y[3]);
     }
-    if (pass == 0 && live) {
-      amax = warp_max(amax);
-      const float before = old > 0 ? *scale : 0.f;
-      float after = fmaxf(before, amax / (I8 ? 127.f : 448.f));
-      if (after < 1.17549435e-38f) after = 0.f;
-      inv = after > 0.f ? 1.f / after : 0.f;
-      __syncwarp();  // every lane has read the old scale
-      if (lane == 0) *scale = after;
-      if (old > 0 && after > before) {
-        for (int j = sub; j < a.block_tokens; j += lt) {  // the block's other slots, 16 codes a lane
-          if (j >= old && j < old + cnt) continue;
-          uint4* p = reinterpret_cast<uint4*>(dst + (int64_t)j * d1 + item * 16);
-          const uint4 w = *p;
-          uint32_t in[4] = {w.x, w.y, w.z, w.w}, out[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t c = (in[e] >> (8 * b)) & 0xFFu;
-              y[b] = (I8 ? (float)(int8_t)c : e4m3_to_float(c)) * before * inv;
-            }
-            out[e] = codes4<I8>(y[0], y[1], y[2], y[3]);
-          }
-          *p = make_uint4(out[0], out[1], out[2], out[3]);
-        }
-      }
-    }
+    *p = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
-template <bool I8>
-__global__ void __launch_bounds__(kBlockThreads) append_blocks_kernel(const __grid_constant__ AppendArgs a) {
-  extern __shared__ float4 table[];
-  __shared__ int32_t s_pos[kTableTokens];
-  const int b = blockIdx.x;
-  if (b >= a.num_kv_blocks) {
-    const int t0 = (b - a.num_kv_blocks) * a.per_block;
-    rows_pass<MODE_NONE, kBlockThreads>(a, t0, min(a.per_block, a.num_rows - t0), table);
-    return;
+// One segment, by the whole block: rows [t0, t0 + cnt) into slots [first + old, ...) of the scale block
+// `blk` of `page`, whose first slot is `first`; pos: the first row's position.
+template <bool I8, bool V, int TURN>
+__device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, int page, int first, int blk, int old,
+                                        int pos, float4* table, BlockShared& sh) {
+  constexpr int threads = 32 * kBlockWarps;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int items = a.head_dim / 16, item = lane % items, lt = 32 / items;
+  int g = 1;  // warps of a head
+  while (g < kBlockWarps && min(cnt, kTableTokens) > g * lt) g *= 2;
+  const int part = warp & (g - 1), sub = part * lt + lane / items;  // this lane's row of a chunk
+  const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
+  const rope::Item it = rope::item_of(item, TURN == kCopy ? 0 : a.f.dim, TURN == kHalves, a.head_dim);
+  const int64_t src_row = V ? a.v0 : a.k0, dst_row = V ? a.vc1 : a.kc1;
+  const bool once = cnt <= kTableTokens;  // the rows of a head fit the lanes' registers
+  // this lane's row of the first chunk, for the head its warp begins with; heads follow by strides
+  const int heads = kBlockWarps / g, h0 = warp / g;
+  const __nv_bfloat16* src = row_ptr<V>(a, t0 + sub, h0);
+  const int64_t src_head = heads * (V ? a.v1 : a.k1);
+  rope::Raw<__nv_bfloat16> raw;
+  float x[16];
+  auto load = [&](int h, int c0) {
+    if (h < a.hk && sub < min(cnt - c0, kTableTokens)) raw.load(src + c0 * src_row, it);
+  };
+  auto fill = [&](int c0) {
+    if (TURN == kCopy) return;
+    const int n = min(cnt - c0, kTableTokens);
+    __syncthreads();  // the last table has been read
+    for (int j = tid; j < n; j += threads)
+      sh.pos[j] = a.positions != nullptr ? __ldg(a.positions + t0 + c0 + j) : pos + c0 + j;
+    __syncthreads();
+    rope::fill_table(table, sh.pos, n, a.f, tid, threads);
+    __syncthreads();
+  };
+  auto turn = [&](int c0) {  // raw -> x
+    raw.values(x);
+    if (TURN != kCopy && it.turned && sub < min(cnt - c0, kTableTokens))
+      rope::turn_item(x, table + sub * stride4, item, nrot, TURN == kHalves);
+  };
+  if (once) load(h0, 0);
+  if (!sound_page(a, page, lane)) return;  // the same for every warp
+  if (once) fill(0);
+  float* scale = scale_ptr<V>(a, page, blk, h0);
+  const int64_t scale_head = heads * (V ? a.vs2 : a.ks2);
+  uint8_t* dst = cache_ptr<V>(a, page, first, h0);
+  const int64_t dst_head = heads * (V ? a.vc2 : a.kc2);
+  int odd = 0;
+#pragma unroll 1
+  for (int h = h0; h < h0 + a.hk; h += heads, odd ^= 1) {  // the same number of rounds for every warp
+    const bool live = h < a.hk;
+    const float before = live && old > 0 ? *scale : 0.f;
+    float top = 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
+      if (!once) {
+        load(h, c0);
+        fill(c0);
+      }
+      turn(c0);
+      if (live && sub < min(cnt - c0, kTableTokens))
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+    }
+    if (once) {  // the next heads' rows
+      src += src_head;
+      load(h + heads, 0);
+    }
+    uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // of values >= 0: order as integers
+    if (g > 1) {  // two buffers: the next heads' maxima are written while these are read
+      if (lane == 0) sh.amax[odd][warp] = amax;
+      __syncthreads();  // and every warp has read the old scale
+      amax = __reduce_max_sync(0xffffffffu, sh.amax[odd][warp - part + (lane & (g - 1))]);
+    }
+    float after = fmaxf(before, __uint_as_float(amax) * (I8 ? 1.f / 127.f : 1.f / 448.f));
+    if (after < 1.17549435e-38f) after = 0.f;
+    const float inv = after > 0.f ? __fdividef(1.f, after) : 0.f;
+    __syncwarp();
+    if (live && lane == 0 && part == 0) *scale = after;
+#pragma unroll 1
+    for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
+      if (!once) {
+        load(h, c0);
+        fill(c0);
+        turn(c0);
+      }
+      if (!live || sub >= min(cnt - c0, kTableTokens)) continue;
+      uint2 code[2];
+      encode_item<I8>(x, inv, code);
+      uint8_t* row = dst + (old + c0 + sub) * dst_row;
+      *reinterpret_cast<uint2*>(row + it.c0) = code[0];
+      *reinterpret_cast<uint2*>(row + it.c1) = code[1];
+    }
+    if (live && old > 0 && after > before)
+      reencode<I8>(dst, dst_row, a.block_tokens, old, cnt, sub, lt * g, item, before, inv);
+    if (!once) src += src_head;
+    scale += scale_head;
+    dst += dst_head;
   }
-  const int window = b % a.num_windows, part = b / a.num_windows;
-  const bool is_v = part >= a.num_head_groups;
-  const int h = (part - (is_v ? a.num_head_groups : 0)) * (kBlockThreads / 32) + (int)(threadIdx.x >> 5);
-  const bool live = h < a.hk;
+}
+
+// The segments that begin in a window.  (K's and V's loops apart: one loop over both would keep both
+// sets of strides in registers.)
+template <bool I8, bool V, int TURN>
+__device__ __forceinline__ void window_segments(const AppendArgs& a, int window, float4* table, BlockShared& sh) {
   const int lane = threadIdx.x & 31, bt = a.block_tokens;
   const int total = min(a.num_rows, __ldg(a.ip + a.batch));
   const int t1 = min((window + 1) * a.per_block, total);
@@ -303,30 +360,41 @@ __global__ void __launch_bounds__(kBlockThreads) append_blocks_kernel(const __gr
     }
     const int in = pl.pos % bt;
     const int cnt = min(min(bt - in, pl.n - pl.i), total - t);
-    if ((pl.i == 0 || in == 0) && pl.page >= 0) {
-      const int slot = pl.pos % a.page_size - in, blk = slot / bt;  // the block's first slot, its number
-      if (is_v) {
-        segment<I8, false>(a, a.v + (int64_t)h * a.v1, a.v0,
-                           a.vc + (int64_t)pl.page * a.vc0 + (int64_t)slot * a.vc1 + (int64_t)h * a.vc2, a.vc1,
-                           a.vsc + (int64_t)pl.page * a.vs0 + (int64_t)blk * a.vs1 + (int64_t)h * a.vs2, t, cnt, in,
-                           pl.pos, live, table, s_pos);
-      } else if (a.f.dim > 0) {
-        segment<I8, true>(a, a.k + (int64_t)h * a.k1, a.k0,
-                          a.kc + (int64_t)pl.page * a.kc0 + (int64_t)slot * a.kc1 + (int64_t)h * a.kc2, a.kc1,
-                          a.ksc + (int64_t)pl.page * a.ks0 + (int64_t)blk * a.ks1 + (int64_t)h * a.ks2, t, cnt, in,
-                          pl.pos, live, table, s_pos);
-      } else {
-        segment<I8, false>(a, a.k + (int64_t)h * a.k1, a.k0,
-                           a.kc + (int64_t)pl.page * a.kc0 + (int64_t)slot * a.kc1 + (int64_t)h * a.kc2, a.kc1,
-                           a.ksc + (int64_t)pl.page * a.ks0 + (int64_t)blk * a.ks1 + (int64_t)h * a.ks2, t, cnt, in,
-                           pl.pos, live, table, s_pos);
-      }
+    if (pl.i == 0 || in == 0) {
+      const int first = pl.pos % a.page_size - in;  // the block's first slot
+      __syncthreads();  // the last segment's shared values have been read
+      segment<I8, V, TURN>(a, t, cnt, pl.page, first, first / bt, in, pl.pos, table, sh);
     }
     t += cnt;
   }
 }
 
+template <bool I8, int TURN>
+__global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(const __grid_constant__ AppendArgs a) {
+  extern __shared__ float4 table[];
+  __shared__ BlockShared sh;
+  // K's windows, then V's (alternating, they would land on alternating SMs: an even number of them)
+  const int b = blockIdx.x;
+  if (b < a.num_windows) {
+    window_segments<I8, false, TURN>(a, b, table, sh);
+  } else if (b < 2 * a.num_windows) {
+    window_segments<I8, true, kCopy>(a, b - a.num_windows, table, sh);
+  } else {
+    const int t0 = (b - 2 * a.num_windows) * a.per_q_block;
+    rows_pass<MODE_NONE, 32 * kBlockWarps>(a, t0, min(a.per_q_block, a.num_rows - t0), table);
+  }
+}
+
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <bool I8>
+int launch_blocks(const AppendArgs& a, int blocks, int smem, cudaStream_t s) {
+  constexpr int threads = 32 * kBlockWarps;
+  if (a.f.dim == 0) append_blocks_kernel<I8, kCopy><<<blocks, threads, smem, s>>>(a);
+  else if (a.f.halves) append_blocks_kernel<I8, kHalves><<<blocks, threads, smem, s>>>(a);
+  else append_blocks_kernel<I8, kInterleaved><<<blocks, threads, smem, s>>>(a);
+  return (int)cudaGetLastError();
+}
 
 }  // namespace
 
@@ -378,23 +446,27 @@ int launch_kv_append(const skv_append_params& p, cudaStream_t s) {
   a.inv_scale = p.kv_dtype == SKV_E4M3 && p.block_tokens == 0 ? 1.f / p.kv_scale : 1.f;
   rope::make_freq(p.rope, false, &a.f);
   const int64_t sms = device_sm_count();
-  // enough windows to fill the SMs several times over, then up to kMaxTokens rows in each
-  a.per_block = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, p.num_rows / (sms * 8)));
   const int table_bytes = a.f.dim * 4;  // of one token
+  const int items = a.head_dim / 16;
   if (p.block_tokens == 0) {
+    a.per_block = rope::tokens_per_block(p.num_rows, (2 * a.hk + a.hq) * items, kRowThreads, kMaxTokens, sms);
     const int blocks = cdiv(p.num_rows, a.per_block), smem = a.per_block * table_bytes;
     if (p.kv_dtype == SKV_BF16) append_rows_kernel<MODE_BF16><<<blocks, kRowThreads, smem, s>>>(a);
     else append_rows_kernel<MODE_E4M3><<<blocks, kRowThreads, smem, s>>>(a);
     return (int)cudaGetLastError();
   }
+  // windows of one row while there are few, then up to a block's tokens (one or two segments each)
+  a.per_block = (int)std::min<int64_t>(std::min(p.block_tokens, kTableTokens),
+                                       std::max<int64_t>(1, p.num_rows / (sms * 2)));
   a.num_windows = cdiv(p.num_rows, a.per_block);
-  a.num_head_groups = cdiv(p.num_kv_heads, kBlockThreads / 32);
-  a.num_kv_blocks = a.num_windows * a.num_head_groups * 2;
-  const int blocks = a.num_kv_blocks + (p.num_q_heads > 0 ? a.num_windows : 0);
-  const int smem = std::max(a.per_block, std::min(p.block_tokens, kTableTokens)) * table_bytes;  // <= 32 KB
-  if (p.kv_dtype == SKV_I8) append_blocks_kernel<true><<<blocks, kBlockThreads, smem, s>>>(a);
-  else append_blocks_kernel<false><<<blocks, kBlockThreads, smem, s>>>(a);
-  return (int)cudaGetLastError();
+  a.per_q_block = 1;
+  int blocks = 2 * a.num_windows;
+  if (a.hq > 0) {
+    a.per_q_block = rope::tokens_per_block(p.num_rows, a.hq * items, 32 * kBlockWarps, kMaxTokens, sms);
+    blocks += cdiv(p.num_rows, a.per_q_block);
+  }
+  const int smem = std::max(a.per_q_block, std::min(p.block_tokens, kTableTokens)) * table_bytes;  // <= 32 KB
+  return p.kv_dtype == SKV_I8 ? launch_blocks<true>(a, blocks, smem, s) : launch_blocks<false>(a, blocks, smem, s);
 }
 
 }  // namespace skv

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 template <typename T>
 int launch(const RopeArgs& a, cudaStream_t s) {
-  const int smem = a.per_block * rope::kMaxPairs * 8;  // <= 16 KB: below the default limit
+  const int smem = a.per_block * a.f.dim * 4;  // <= 16 KB: below the default limit
   rope_kernel<T><<<(a.tokens + a.per_block - 1) / a.per_block, kThreads, smem, s>>>(a);
   return (int)cudaGetLastError();
 }
@@ -125,9 +125,7 @@ int launch_rope(const skv_rope_params& p, cudaStream_t s) {
   const bool in_place = (p.num_q_heads == 0 || p.q == p.q_out) && (p.num_k_heads == 0 || p.k == p.k_out);
   a.items = in_place ? p.rope.dim / 16 : (p.head_dim + 15) / 16;  // in place: copied values stay where they are
   if (a.items == 0) return 0;
-  // enough blocks to fill the SMs several times over, then as many tokens per block as fit
-  const int64_t want = (int64_t)device_sm_count() * 8;
-  a.per_block = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, p.num_tokens / want));
+  a.per_block = rope::tokens_per_block(p.num_tokens, (a.hq + a.hk) * a.items, kThreads, kMaxTokens, device_sm_count());
   return p.dtype == SKV_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);
 }
 

@@ -46,17 +46,18 @@ def _entry(name: str, args: int):
     return ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * args)((name, _lib))
 
 
+_addressof, _char = ctypes.addressof, ctypes.c_char
 _call_rope, _call_append = _entry("skv_rope_apply", 2), _entry("skv_paged_kv_append", 2)
 _call_scaled, _call_prompt = _entry("skv_paged_attn_scaled_fwd", 4), _entry("skv_prompt_attn_fwd", 4)
 
-torch = _bf16 = _f32 = _i32 = _cache_codes = _raw_stream = _cuda_device = None
+torch = _bf16 = _f32 = _i32 = _cache_codes = _raw_stream = _cuda_device = _contiguous = None
 
 
 def _init() -> None:
     """Imports torch on the first call (planning alone needs numpy only)."""
-    global torch, _bf16, _f32, _i32, _cache_codes, _raw_stream, _cuda_device
+    global torch, _bf16, _f32, _i32, _cache_codes, _raw_stream, _cuda_device, _contiguous
     import torch as t
-    _bf16, _f32, _i32 = t.bfloat16, t.float32, t.int32
+    _bf16, _f32, _i32, _contiguous = t.bfloat16, t.float32, t.int32, t.contiguous_format
     _cache_codes = {t.bfloat16: BF16, t.float8_e4m3fn: E4M3, t.uint8: E4M3, t.int8: I8}
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or \
         (lambda i: t.cuda.current_stream(i).cuda_stream)
@@ -75,15 +76,9 @@ def _device_index(t) -> int:
     return i
 
 
-def _same_device(dev: int, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            _bad(f"{name} is on {t.device}, expected cuda:{dev}")
-
-
 def _index(name: str, t, n: int, dev: int) -> int:
     """Address of a contiguous int32 vector of n entries (n < 0: any) on the device."""
-    if t.dtype is not _i32 or t.dim() != 1 or (n >= 0 and t.shape[0] != n) or not t.is_contiguous():
+    if t.dtype is not _i32 or t.dim() != 1 or (n >= 0 and t.numel() != n) or not t.is_contiguous():
         _bad(f"{name} must be a contiguous int32 vector" + ("" if n < 0 else f" of {n} entries"))
     if t.get_device() != dev:
         _bad(f"{name} is on {t.device}, expected cuda:{dev}")
@@ -92,13 +87,24 @@ def _index(name: str, t, n: int, dev: int) -> int:
 
 def _rows(name: str, t, dtype, rows: int, dim: int, dev: int):
     """(heads, address, token stride, head stride) of a [rows, heads, dim] tensor."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3:
-        _bad(f"{name} must be a {dtype} tensor [{rows}, heads, {dim}] on cuda:{dev}")
-    n, heads, d = t.shape
+    try:
+        n, heads, d = t.shape
+    except ValueError:
+        n = heads = d = -1
+    if n != rows or d != dim or t.dtype is not dtype or t.get_device() != dev:
+        _bad(f"{name} must be a {dtype} tensor [{rows}, heads, {dim}] on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+             f"on {t.device}")
     s0, s1, s2 = t.stride()
-    if n != rows or d != dim or (s2 != 1 and n * heads * d):
-        _bad(f"{name} must be [{rows}, heads, {dim}] with contiguous heads, got {tuple(t.shape)}")
+    if s2 != 1 and n * heads * d:
+        _bad(f"{name} must have contiguous heads")
     return heads, t.data_ptr(), s0, s1
+
+
+def _like(t, heads: int):
+    """A new tensor of t's shape and dtype, and its (heads, address, token stride, head stride)."""
+    out = torch.empty_like(t, memory_format=_contiguous)
+    d = t.shape[2]
+    return out, (heads, out.data_ptr(), heads * d, d)
 
 
 class _Launch:
@@ -139,8 +145,10 @@ def _freqs(rope_dim: int, rope_layout: str, inv_freq):
     if inv_freq is None or rope_dim <= 0:
         return layout, 0, None
     f = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    if f.ndim != 1 or 2 * f.shape[0] != rope_dim:
+    if f.ndim != 1 or 2 * f.size != rope_dim:
         _bad(f"inv_freq must hold rope_dim / 2 = {rope_dim // 2} frequencies")
+    if f.flags.writeable:  # the address, by the quicker way where the array allows it
+        return layout, _addressof(_char.from_buffer(f)), f
     return layout, f.__array_interface__["data"][0], f
 
 
@@ -192,16 +200,18 @@ def rope_apply(q, k, positions, *, rope_dim: Optional[int] = None, rope_theta: f
     qi = qo = ki = ko = _NO_ROWS
     if q is not None:
         qi = _rows("q", q, dtype, tokens, dim, dev)
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        qo = _rows("q_out", q_out, dtype, tokens, dim, dev)
         hq = qi[0]
+        if q_out is None:
+            q_out, qo = _like(q, hq)
+        else:
+            qo = _rows("q_out", q_out, dtype, tokens, dim, dev)
     if k is not None:
         ki = _rows("k", k, dtype, tokens, dim, dev)
-        if k_out is None:
-            k_out = k.new_empty(k.shape)
-        ko = _rows("k_out", k_out, dtype, tokens, dim, dev)
         hk = ki[0]
+        if k_out is None:
+            k_out, ko = _like(k, hk)
+        else:
+            ko = _rows("k_out", k_out, dtype, tokens, dim, dev)
     if qo[0] != hq or ko[0] != hk or (q is None and q_out is not None) or (k is None and k_out is not None):
         _bad("q_out and k_out must have the shapes of q and k")
     rope_dim = dim if rope_dim is None else rope_dim
@@ -219,9 +229,10 @@ def _caches(k_cache, v_cache, dim: int, num_pages, dev: int):
     code = _cache_codes.get(k_cache.dtype)
     if code is None or v_cache.dtype is not k_cache.dtype:
         _bad("caches must both be bfloat16, float8_e4m3fn or int8")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         _bad("the caches must both be [num_pages, P, Hk, D]")
-    held, page, hk, d = k_cache.shape
+    held, page, hk, d = shape
     ks, vs = k_cache.stride(), v_cache.stride()
     if d != dim or ks[3] != 1 or vs[3] != 1:
         _bad(f"the caches must be [num_pages, P, Hk, {dim}] with contiguous heads")
@@ -235,11 +246,14 @@ def _caches(k_cache, v_cache, dim: int, num_pages, dev: int):
 
 def _scales(k_scale, v_scale, pages: int, page: int, hk: int, dev: int) -> int:
     """Tokens that share a scale in the scale tensors [num_pages, blocks per page, Hk] float32."""
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is None or t.dtype is not _f32 or t.dim() != 3 or t.get_device() != dev:
-            _bad(f"{name} must be float32 [num_pages, blocks per page, {hk}] on cuda:{dev}")
-    n, blocks, heads = k_scale.shape
-    if v_scale.shape != k_scale.shape or n < pages or heads != hk or blocks < 1 or page % blocks:
+    if k_scale is None or v_scale is None:
+        _bad("k_scale and v_scale come together")
+    shape = k_scale.shape
+    if len(shape) != 3 or v_scale.shape != shape or k_scale.dtype is not _f32 or v_scale.dtype is not _f32 \
+            or k_scale.get_device() != dev or v_scale.get_device() != dev:
+        _bad(f"k_scale and v_scale must be float32 [num_pages, blocks per page, {hk}] on cuda:{dev}")
+    n, blocks, heads = shape
+    if n < pages or heads != hk or blocks < 1 or page % blocks:
         _bad(f"k_scale and v_scale must be float32 [num_pages, blocks per page, {hk}] with whole blocks of tokens")
     return page // blocks
 
@@ -272,9 +286,9 @@ def paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices
     code, pages, page, hk, ks, vs = _caches(k_cache, v_cache, dim, num_pages, dev)
     if ki[0] != hk or vi[0] != hk:
         _bad(f"k, v and the caches must have the same heads, got {ki[0]}, {vi[0]} and {hk}")
-    if append_indptr.dim() != 1 or append_indptr.shape[0] < 1:
+    batch = append_indptr.numel() - 1
+    if batch < 0:
         _bad("append_indptr must be a contiguous int32 vector")
-    batch = append_indptr.shape[0] - 1
     block, kp, vp, kss, vss = 0, 0, 0, _NO_ROWS, _NO_ROWS
     if k_scale is not None or v_scale is not None:
         block = _scales(k_scale, v_scale, pages, page, hk, dev)
@@ -283,8 +297,9 @@ def paged_kv_append(k, v, k_cache, v_cache, append_indptr, kv_indptr, kv_indices
     if q is not None:
         qi = _rows("q", q, _bf16, rows, dim, dev)
         if q_out is None:
-            q_out = q.new_empty(q.shape)
-        qo = _rows("q_out", q_out, _bf16, rows, dim, dev)
+            q_out, qo = _like(q, qi[0])
+        else:
+            qo = _rows("q_out", q_out, _bf16, rows, dim, dev)
     if qo[0] != qi[0] or (q is None and q_out is not None):
         _bad("q_out must have the shape of q")
     layout, freq, keep = _freqs(rope_dim, rope_layout, inv_freq)
@@ -305,7 +320,10 @@ def _outputs(q, total_q: int, hq: int, dim: int, o_dtype, o_out, lse_out, dev: i
     """(o, its dtype code, lse), allocated unless given."""
     if o_out is None:
         dtype = o_dtype or _f32
-        o = q.new_empty((total_q, hq, dim), dtype=dtype)
+        if dtype is _bf16:
+            o = torch.empty_like(q, memory_format=_contiguous)
+        else:
+            o = q.new_empty((total_q, hq, dim), dtype=dtype)
     else:
         o, dtype = o_out, o_out.dtype
         if tuple(o.shape) != (total_q, hq, dim) or not o.is_contiguous() or o.get_device() != dev:

@@ -17,8 +17,8 @@
 // rows from registers while the next heads' rows are on their way.  Segments of more than 64 tokens
 // are read twice.  One owner per (block, head): no atomics, results do not depend on order.  Window w
 // of the grid takes the segments that begin among its rows; the last blocks of the grid rotate Q.
-// (One warp per head, two passes over its rows: 93 us for 20 k tokens in blocks of 64; eight warps for
-// two heads, each with its own search and table: 121 us; this form: SEGMENT_US us.)
+// (One warp per head, two passes over its rows: 93 us for 18 k tokens, 8 heads of 128, blocks of 64;
+// eight warps for two heads, each with its own search and table: 121 us; this form: 52 us.)
 #include "rope.cuh"
 
 #include <cuda_fp8.h>
@@ -33,6 +33,7 @@ using rope::Freq;
 
 constexpr int kRowThreads = 256;
 constexpr int kBlockWarps = 16;  // block kernel
+constexpr int kMaxPairs = 64;    // head_dim <= 128
 constexpr int kMaxTokens = 16;   // tokens per block of threads, row kernel
 constexpr int kTableTokens = 64; // tokens whose tables are held at once, block kernel
 
@@ -60,7 +61,7 @@ struct AppendArgs {
   int batch, num_rows, num_pages, page_size, hk, hq, head_dim, block_tokens;
   int per_block;        // rows of a window
   int per_q_block;      // rows of a block of threads that rotates Q beside the block kernel
-  int num_windows;
+  int num_windows, stripe, num_kv_blocks;
   float inv_scale;
   Freq f;
 };
@@ -135,6 +136,7 @@ __device__ __forceinline__ void encode_item(const float (&x)[16], float inv, uin
 template <int MODE, int THREADS>
 __device__ __forceinline__ void rows_pass(const AppendArgs& a, int t0, int n, float4* table) {
   __shared__ int32_t s_pos[kMaxTokens], s_page[kMaxTokens], s_slot[kMaxTokens], s_ok[kMaxTokens];
+  __shared__ uint64_t turns[kMaxPairs];
   const int tid = threadIdx.x, lane = tid & 31;
   const int total = min(a.num_rows, __ldg(a.ip + a.batch));
   n = min(n, total - t0);
@@ -143,7 +145,7 @@ __device__ __forceinline__ void rows_pass(const AppendArgs& a, int t0, int n, fl
   const int kv = MODE == MODE_NONE ? 0 : 2 * a.hk, heads = kv + a.hq;
   const int rows_per_pass = THREADS / items;
   const int item = tid % items;
-  const rope::Item it = rope::item_of(item, a.f.dim, a.f.halves, a.head_dim);
+  const rope::Item it = rope::item_of(item, a.f.dim, a.head_dim);
   auto src = [&](int tk, int h) {
     const int64_t t = t0 + tk;
     return h < kv ? (h < a.hk ? a.k + t * a.k0 + (int64_t)h * a.k1 : a.v + t * a.v0 + (int64_t)(h - a.hk) * a.v1)
@@ -161,8 +163,9 @@ __device__ __forceinline__ void rows_pass(const AppendArgs& a, int t0, int n, fl
       s_ok[j] = pl.ok;
     }
   }
+  rope::stage_turns(turns, a.f, tid, THREADS);
   __syncthreads();
-  rope::fill_table(table, s_pos, n, a.f, tid, THREADS);
+  rope::fill_table(table, s_pos, n, turns, a.f.dim, a.f.mscale, a.f.halves, tid, THREADS);
   __syncthreads();
   while (tok < n) {
     const int tk = tok, hd = h;
@@ -203,6 +206,7 @@ __global__ void __launch_bounds__(kRowThreads) append_rows_kernel(const __grid_c
 
 // Shared memory of the block kernel beside the table.
 struct BlockShared {
+  uint64_t turns[kMaxPairs];
   int32_t pos[kTableTokens];
   uint32_t amax[2][kBlockWarps];
 };
@@ -256,7 +260,7 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
   while (g < kBlockWarps && min(cnt, kTableTokens) > g * lt) g *= 2;
   const int part = warp & (g - 1), sub = part * lt + lane / items;  // this lane's row of a chunk
   const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
-  const rope::Item it = rope::item_of(item, TURN == kCopy ? 0 : a.f.dim, TURN == kHalves, a.head_dim);
+  const rope::Item it = rope::item_of(item, TURN == kCopy ? 0 : a.f.dim, a.head_dim);
   const int64_t src_row = V ? a.v0 : a.k0, dst_row = V ? a.vc1 : a.kc1;
   const bool once = cnt <= kTableTokens;  // the rows of a head fit the lanes' registers
   // this lane's row of the first chunk, for the head its warp begins with; heads follow by strides
@@ -275,7 +279,7 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     for (int j = tid; j < n; j += threads)
       sh.pos[j] = a.positions != nullptr ? __ldg(a.positions + t0 + c0 + j) : pos + c0 + j;
     __syncthreads();
-    rope::fill_table(table, sh.pos, n, a.f, tid, threads);
+    rope::fill_table(table, sh.pos, n, sh.turns, a.f.dim, a.f.mscale, TURN == kHalves, tid, threads);
     __syncthreads();
   };
   auto turn = [&](int c0) {  // raw -> x
@@ -348,6 +352,7 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
 // sets of strides in registers.)
 template <bool I8, bool V, int TURN>
 __device__ __forceinline__ void window_segments(const AppendArgs& a, int window, float4* table, BlockShared& sh) {
+  if (TURN != kCopy) rope::stage_turns(sh.turns, a.f, threadIdx.x, 32 * kBlockWarps);
   const int lane = threadIdx.x & 31, bt = a.block_tokens;
   const int total = min(a.num_rows, __ldg(a.ip + a.batch));
   const int t1 = min((window + 1) * a.per_block, total);
@@ -373,14 +378,14 @@ template <bool I8, int TURN>
 __global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(const __grid_constant__ AppendArgs a) {
   extern __shared__ float4 table[];
   __shared__ BlockShared sh;
-  // K's windows, then V's (alternating, they would land on alternating SMs: an even number of them)
-  const int b = blockIdx.x;
-  if (b < a.num_windows) {
-    window_segments<I8, false, TURN>(a, b, table, sh);
-  } else if (b < 2 * a.num_windows) {
-    window_segments<I8, true, kCopy>(a, b - a.num_windows, table, sh);
+  // stripes of one block per SM, K's and V's in turns: an SM gets as many of the one as of the other
+  const int b = blockIdx.x, stripe = b / a.stripe, window = (stripe >> 1) * a.stripe + b % a.stripe;
+  if (b < a.num_kv_blocks) {
+    if (window >= a.num_windows) return;
+    if (stripe & 1) window_segments<I8, true, kCopy>(a, window, table, sh);
+    else window_segments<I8, false, TURN>(a, window, table, sh);
   } else {
-    const int t0 = (b - 2 * a.num_windows) * a.per_q_block;
+    const int t0 = (b - a.num_kv_blocks) * a.per_q_block;
     rows_pass<MODE_NONE, 32 * kBlockWarps>(a, t0, min(a.per_q_block, a.num_rows - t0), table);
   }
 }
@@ -457,10 +462,12 @@ int launch_kv_append(const skv_append_params& p, cudaStream_t s) {
   }
   // windows of one row while there are few, then up to a block's tokens (one or two segments each)
   a.per_block = (int)std::min<int64_t>(std::min(p.block_tokens, kTableTokens),
-                                       std::max<int64_t>(1, p.num_rows / (sms * 2)));
+                                       std::max<int64_t>(1, p.num_rows / (sms * 4)));
   a.num_windows = cdiv(p.num_rows, a.per_block);
   a.per_q_block = 1;
-  int blocks = 2 * a.num_windows;
+  a.stripe = (int)std::min<int64_t>(sms, a.num_windows);
+  a.num_kv_blocks = 2 * a.stripe * cdiv(a.num_windows, a.stripe);
+  int blocks = a.num_kv_blocks;
   if (a.hq > 0) {
     a.per_q_block = rope::tokens_per_block(p.num_rows, a.hq * items, 32 * kBlockWarps, kMaxTokens, sms);
     blocks += cdiv(p.num_rows, a.per_q_block);

@@ -34,12 +34,13 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float4 table[];
   __shared__ int32_t pos[kMaxTokens];
+  __shared__ uint64_t turns[rope::kMaxPairs];
   const int tid = threadIdx.x;
   const int t0 = blockIdx.x * a.per_block, n = min(a.per_block, a.tokens - t0);
   const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
   const int rows_per_pass = kThreads / a.items;
   const int item = tid % a.items;
-  const rope::Item it = rope::item_of(item, a.f.dim, a.f.halves, a.head_dim);
+  const rope::Item it = rope::item_of(item, a.f.dim, a.head_dim);
   const int heads = a.hq + a.hk, rows = n * heads;
   int row = tid / a.items;
   const bool active = row < rows_per_pass;
@@ -73,9 +74,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
   };
   fetch();
-  if (tid < n) pos[tid] = a.positions[t0 + tid];
+  if (tid < n) pos[tid] = a.f.dim > 0 ? a.positions[t0 + tid] : 0;
+  rope::stage_turns(turns, a.f, tid, kThreads);
   __syncthreads();
-  rope::fill_table(table, pos, n, a.f, tid, kThreads);
+  rope::fill_table(table, pos, n, turns, a.f.dim, a.f.mscale, a.f.halves, tid, kThreads);
   __syncthreads();
   if (!active) return;
   while (tks[0] < n) {
@@ -123,7 +125,8 @@ int launch_rope(const skv_rope_params& p, cudaStream_t s) {
   a.head_dim = p.head_dim;
   rope::make_freq(p.rope, p.inverse != 0, &a.f);
   const bool in_place = (p.num_q_heads == 0 || p.q == p.q_out) && (p.num_k_heads == 0 || p.k == p.k_out);
-  a.items = in_place ? p.rope.dim / 16 : (p.head_dim + 15) / 16;  // in place: copied values stay where they are
+  // in place, copied values stay where they are
+  a.items = p.rope.dim / 16 + (in_place ? 0 : ((p.head_dim - p.rope.dim) / 8 + 1) / 2);
   if (a.items == 0) return 0;
   a.per_block = rope::tokens_per_block(p.num_tokens, (a.hq + a.hk) * a.items, kThreads, kMaxTokens, device_sm_count());
   return p.dtype == SKV_F32 ? launch<float>(a, s) : launch<__nv_bfloat16>(a, s);

@@ -76,21 +76,33 @@ __device__ __forceinline__ float2 cos_sin(int32_t pos, uint64_t turns, float msc
   return make_float2(((quad == 1 || quad == 2) ? -cc : cc) * mscale, ((quad & 2) ? -ss : ss) * mscale);
 }
 
-// A row of D values is cut into items of 16: item i < dim/16 holds eight whole pairs (two 8-value
-// chunks: i and i + dim/16 for halves, 2i and 2i+1 for interleaved pairs), later items are copied.
-// The table of a token holds item i's pairs (2j, 2j+1) as one float4 at [j][i], so the lanes of a
-// row read consecutive 16-byte words.
+// A row of D values is cut into items of 16, two chunks of 8 half a part of the row apart, so that the
+// lanes of a row read and write consecutive chunks (with 16 consecutive values a lane, each 32-byte
+// sector was written by two instructions).  Item i < dim/16 holds chunks i and dim/16 + i and
+// with them eight whole pairs: (x[p], x[8+p]) for halves, (x[2p], x[2p+1]) for interleaved pairs, four in
+// each chunk.  Later items are copied.  The table of a token holds item i's pairs (2j, 2j+1) as one
+// float4 at [j][i], so the lanes of a row read consecutive 16-byte words.
 __device__ __forceinline__ int table_float4s(int dim) { return dim / 4; }
 
+// Block-wide: the frequencies into shared memory.  (Lanes that index the parameter bank apart are served
+// one after another; once a block that is bearable, once a table entry it is not.)
+__device__ __forceinline__ void stage_turns(uint64_t* turns, const Freq& f, int tid, int threads) {
+  for (int p = tid; p < f.dim / 2; p += threads) turns[p] = f.turns[p];
+}
+
 // Block-wide: the table of `n` tokens whose positions are pos[0..n).
-__device__ __forceinline__ void fill_table(float4* table, const int32_t* pos, int n, const Freq& f, int tid,
-                                           int threads) {
-  const int half = f.dim / 2, items = f.dim / 16;
+__device__ __forceinline__ void fill_table(float4* table, const int32_t* pos, int n, const uint64_t* turns, int dim,
+                                           float mscale, bool halves, int tid, int threads) {
+  const int half = dim / 2, items = dim / 16;
   if (half == 0) return;  // nothing turns
   float2* t2 = reinterpret_cast<float2*>(table);
   for (int x = tid; x < n * half; x += threads) {
     const int tok = x / half, p = x - tok * half;
-    t2[tok * half + (((p & 7) >> 1) * items + (p >> 3)) * 2 + (p & 1)] = cos_sin(pos[tok], f.turns[p], f.mscale);
+    // halves: pair p is number p % 8 of item p / 8; interleaved: of chunk p / 4, which is the item's first or
+    // second one
+    const int second = !halves && p >= 4 * items, i = halves ? p >> 3 : (p >> 2) - (second ? items : 0);
+    const int j = halves ? (p & 7) >> 1 : 2 * second + ((p & 3) >> 1);
+    t2[tok * half + (j * items + i) * 2 + (p & 1)] = cos_sin(pos[tok], turns[p], mscale);
   }
 }
 
@@ -99,12 +111,12 @@ struct Item {
   int c0, c1;
   bool turned, two;
 };
-__device__ __forceinline__ Item item_of(int i, int dim, int halves, int head_dim) {
+__device__ __forceinline__ Item item_of(int i, int dim, int head_dim) {
   Item it;
-  const int nrot = dim / 16;
+  const int nrot = dim / 16, rest = ((head_dim - dim) / 8 + 1) / 2;  // items turned and copied
   it.turned = i < nrot;
-  it.c0 = (it.turned && halves) ? i * 8 : i * 16;
-  it.c1 = (it.turned && halves) ? dim / 2 + i * 8 : i * 16 + 8;
+  it.c0 = it.turned ? i * 8 : dim + (i - nrot) * 8;
+  it.c1 = it.c0 + (it.turned ? nrot : rest) * 8;
   it.two = it.c1 < head_dim;
   return it;
 }

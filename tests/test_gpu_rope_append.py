@@ -104,6 +104,18 @@ def test_rope_strided_in_place_and_inverse(layout):
     assert bool(torch.all((lhs - rhs).abs() <= bound))
 
 
+def test_rope_copies_without_positions():
+    """The C entry needs no positions when nothing turns."""
+    import ctypes
+    x = _bf16(np.random.default_rng(3), 9, 3, 64)
+    out = torch.zeros_like(x)
+    p = skv.RopeParams(q=x.data_ptr(), q_out=out.data_ptr(), q_stride=x.stride()[:2], q_out_stride=out.stride()[:2],
+                       num_tokens=9, num_q_heads=3, head_dim=64, dtype=skv.BF16, rope=skv.Rope(0, 0, 1e4, None, 1.0))
+    assert skv._rope_apply(ctypes.byref(p), torch.cuda.current_stream().cuda_stream) == skv.OK
+    torch.cuda.synchronize()
+    assert torch.equal(out, x)
+
+
 def test_rope_no_tokens():
     q, _ = skv.rope_apply(torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV), None, _i32([]))
     assert q.shape == (0, 4, 64)

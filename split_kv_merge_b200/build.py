@@ -4,14 +4,18 @@
 
 Each .cu under csrc/ compiles to _build/<name>.o (skipped when newer than its sources and the
 headers), then everything links into split_kv_merge_b200/libsplitkv.so with the CUDA runtime
-linked statically.  The oracle is pure Python/numpy and needs no build step.
+linked statically.  csrc/binding.cpp becomes split_kv_merge_b200/_serving.so, the Python extension of
+the serving operators, against torch's libraries and libsplitkv.so.  The oracle is pure Python/numpy
+and needs no build step.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsplitkv.so")
+BINDING = os.path.join(PKG, "_serving.so")
+CXX = os.environ.get("CXX", "g++")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -55,7 +61,29 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _binding(force)
     return LIB
+
+
+def _binding(force: bool) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    inputs = [src, __file__, os.path.join(ROOT, "include", "splitkv.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, inputs)):
+        return BINDING
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the Python binding needs torch's headers")
+    torch = os.path.dirname(spec.origin)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", BINDING,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch, "include"), "-isystem",
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", PKG, "-lsplitkv", "-Wl,-rpath,$ORIGIN"]  # torch's own libraries are loaded before it
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -18,7 +18,7 @@
 // are read twice.  One owner per (block, head): no atomics, results do not depend on order.  Window w
 // of the grid takes the segments that begin among its rows; the last blocks of the grid rotate Q.
 // (One warp per head, two passes over its rows: 93 us for 18 k tokens, 8 heads of 128, blocks of 64;
-// eight warps for two heads, each with its own search and table: 121 us; this form: 52 us.)
+// eight warps for two heads, each with its own search and table: 121 us; this form: 43 us.)
 #include "rope.cuh"
 
 #include <cuda_fp8.h>
@@ -82,17 +82,19 @@ __device__ __forceinline__ int find_request(const int32_t* ip, int batch, int t,
 // Where row t goes (warp-collective).  ok: the row belongs to a request of a sound table.  The page
 // id is as the table has it (checked by sound_page, so that its load can be in flight meanwhile).
 struct Place {
-  int r, i, n, pos, page;
+  int i, n, pos, page;
+  int64_t first_page;  // the request's first entry of kv_indices
   bool ok;
 };
 __device__ __forceinline__ Place find_place(const AppendArgs& a, int t, int lane) {
   Place pl;
-  pl.r = find_request(a.ip, a.batch, t, lane);
-  const int row0 = __ldg(a.ip + pl.r);
+  const int r = find_request(a.ip, a.batch, t, lane);
+  const int row0 = __ldg(a.ip + r);
   pl.i = t - row0;
-  pl.n = __ldg(a.ip + pl.r + 1) - row0;
-  const int p0 = __ldg(a.kv_indptr + pl.r), np = __ldg(a.kv_indptr + pl.r + 1) - p0;
-  const int64_t len = np > 0 ? (int64_t)(np - 1) * a.page_size + __ldg(a.last + pl.r) : 0;
+  pl.n = __ldg(a.ip + r + 1) - row0;
+  const int p0 = __ldg(a.kv_indptr + r), np = __ldg(a.kv_indptr + r + 1) - p0;
+  const int64_t len = np > 0 ? (int64_t)(np - 1) * a.page_size + __ldg(a.last + r) : 0;
+  pl.first_page = p0;
   pl.page = -1;
   pl.ok = pl.i >= 0 && pl.i < pl.n && len >= pl.n && len <= (int64_t)np * a.page_size && len <= INT32_MAX;
   pl.pos = pl.ok ? (int)len - pl.n + pl.i : 0;
@@ -249,8 +251,9 @@ __device__ __noinline__ void reencode(uint8_t* dst, int64_t row, int tokens, int
 }
 
 // One segment, by the whole block: rows [t0, t0 + cnt) into slots [first + old, ...) of the scale block
-// `blk` of `page`, whose first slot is `first`; pos: the first row's position.
-template <bool I8, bool V, int TURN>
+// `blk` of `page`, whose first slot is `first`; pos: the first row's position.  ONCE: the segment is one
+// chunk of rows, which stay in the lanes' registers.
+template <bool I8, bool V, int TURN, bool ONCE>
 __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, int page, int first, int blk, int old,
                                         int pos, float4* table, BlockShared& sh) {
   constexpr int threads = 32 * kBlockWarps;
@@ -262,16 +265,13 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
   const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
   const rope::Item it = rope::item_of(item, TURN == kCopy ? 0 : a.f.dim, a.head_dim);
   const int64_t src_row = V ? a.v0 : a.k0, dst_row = V ? a.vc1 : a.kc1;
-  const bool once = cnt <= kTableTokens;  // the rows of a head fit the lanes' registers
   // this lane's row of the first chunk, for the head its warp begins with; heads follow by strides
   const int heads = kBlockWarps / g, h0 = warp / g;
   const __nv_bfloat16* src = row_ptr<V>(a, t0 + sub, h0);
   const int64_t src_head = heads * (V ? a.v1 : a.k1);
   rope::Raw<__nv_bfloat16> raw;
   float x[16];
-  auto load = [&](int h, int c0) {
-    if (h < a.hk && sub < min(cnt - c0, kTableTokens)) raw.load(src + c0 * src_row, it);
-  };
+  auto mine = [&](int c0) { return sub < (ONCE ? cnt : min(cnt - c0, kTableTokens)); };
   auto fill = [&](int c0) {
     if (TURN == kCopy) return;
     const int n = min(cnt - c0, kTableTokens);
@@ -282,38 +282,50 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     rope::fill_table(table, sh.pos, n, sh.turns, a.f.dim, a.f.mscale, TURN == kHalves, tid, threads);
     __syncthreads();
   };
-  auto turn = [&](int c0) {  // raw -> x
+  auto turn = [&]() {  // raw -> x, for a lane with a row
     raw.values(x);
-    if (TURN != kCopy && it.turned && sub < min(cnt - c0, kTableTokens))
-      rope::turn_item(x, table + sub * stride4, item, nrot, TURN == kHalves);
+    if (TURN != kCopy && it.turned) rope::turn_item(x, table + sub * stride4, item, nrot, TURN == kHalves);
   };
-  if (once) load(h0, 0);
+  if (ONCE && h0 < a.hk && mine(0)) raw.load(src, it);
   if (!sound_page(a, page, lane)) return;  // the same for every warp
-  if (once) fill(0);
+  if (ONCE) fill(0);
   float* scale = scale_ptr<V>(a, page, blk, h0);
   const int64_t scale_head = heads * (V ? a.vs2 : a.ks2);
   uint8_t* dst = cache_ptr<V>(a, page, first, h0);
   const int64_t dst_head = heads * (V ? a.vc2 : a.kc2);
+  auto store = [&](int c0, float inv) {
+    uint2 code[2];
+    encode_item<I8>(x, inv, code);
+    uint8_t* row = dst + (old + c0 + sub) * dst_row;
+    *reinterpret_cast<uint2*>(row + it.c0) = code[0];
+    *reinterpret_cast<uint2*>(row + it.c1) = code[1];
+  };
+  auto largest = [&](float top) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+    return top;
+  };
   int odd = 0;
 #pragma unroll 1
   for (int h = h0; h < h0 + a.hk; h += heads, odd ^= 1) {  // the same number of rounds for every warp
     const bool live = h < a.hk;
     const float before = live && old > 0 ? *scale : 0.f;
     float top = 0.f;
-#pragma unroll 1
-    for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
-      if (!once) {
-        load(h, c0);
-        fill(c0);
+    if constexpr (ONCE) {
+      if (live && mine(0)) {
+        turn();
+        top = largest(0.f);
+        if (h + heads < a.hk) raw.load(src += src_head, it);  // the next heads' rows
       }
-      turn(c0);
-      if (live && sub < min(cnt - c0, kTableTokens))
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
-    }
-    if (once) {  // the next heads' rows
-      src += src_head;
-      load(h + heads, 0);
+    } else {
+#pragma unroll 1
+      for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
+        fill(c0);
+        if (!live || !mine(c0)) continue;
+        raw.load(src + c0 * src_row, it);
+        turn();
+        top = largest(top);
+      }
     }
     uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // of values >= 0: order as integers
     if (g > 1) {  // two buffers: the next heads' maxima are written while these are read
@@ -326,55 +338,69 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     const float inv = after > 0.f ? __fdividef(1.f, after) : 0.f;
     __syncwarp();
     if (live && lane == 0 && part == 0) *scale = after;
+    if constexpr (ONCE) {
+      if (live && mine(0)) store(0, inv);
+    } else {
 #pragma unroll 1
-    for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
-      if (!once) {
-        load(h, c0);
+      for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
         fill(c0);
-        turn(c0);
+        if (!live || !mine(c0)) continue;
+        raw.load(src + c0 * src_row, it);
+        turn();
+        store(c0, inv);
       }
-      if (!live || sub >= min(cnt - c0, kTableTokens)) continue;
-      uint2 code[2];
-      encode_item<I8>(x, inv, code);
-      uint8_t* row = dst + (old + c0 + sub) * dst_row;
-      *reinterpret_cast<uint2*>(row + it.c0) = code[0];
-      *reinterpret_cast<uint2*>(row + it.c1) = code[1];
+      src += src_head;
     }
     if (live && old > 0 && after > before)
       reencode<I8>(dst, dst_row, a.block_tokens, old, cnt, sub, lt * g, item, before, inv);
-    if (!once) src += src_head;
     scale += scale_head;
     dst += dst_head;
   }
 }
 
 // The segments that begin in a window.  (K's and V's loops apart: one loop over both would keep both
-// sets of strides in registers.)
-template <bool I8, bool V, int TURN>
+// sets of strides in registers.  LONG: blocks may hold more than kTableTokens tokens.)
+template <bool I8, bool V, int TURN, bool LONG>
 __device__ __forceinline__ void window_segments(const AppendArgs& a, int window, float4* table, BlockShared& sh) {
   if (TURN != kCopy) rope::stage_turns(sh.turns, a.f, threadIdx.x, 32 * kBlockWarps);
   const int lane = threadIdx.x & 31, bt = a.block_tokens;
   const int total = min(a.num_rows, __ldg(a.ip + a.batch));
-  const int t1 = min((window + 1) * a.per_block, total);
-  for (int t = window * a.per_block; t < t1;) {
-    const Place pl = find_place(a, t, lane);
-    if (!pl.ok) {  // the rest of a malformed request (or of the table) is skipped
-      if (pl.i < 0 || pl.i >= pl.n) return;
-      t += pl.n - pl.i;
-      continue;
+  const int t1 = (int)min((window + 1) * (int64_t)a.per_block, (int64_t)total);
+  int t = window * a.per_block;
+  if (t >= t1) return;
+  Place pl = find_place(a, t, lane);
+  while (true) {
+    int cnt = pl.n - pl.i, page = pl.page;
+    if (pl.ok) {
+      const int in = pl.pos % bt;
+      cnt = min(min(bt - in, cnt), total - t);
+      // the request's next segment needs its page id only; that load runs beside this segment
+      const bool more = pl.i + cnt < pl.n && t + cnt < t1;
+      if (more) pl.page = __ldg(a.kv_indices + pl.first_page + (pl.pos + cnt) / a.page_size);
+      if (pl.i == 0 || in == 0) {
+        const int first = pl.pos % a.page_size - in;  // the block's first slot
+        __syncthreads();  // the last segment's shared values have been read
+        if (LONG && cnt > kTableTokens)
+          segment<I8, V, TURN, false>(a, t, cnt, page, first, first / bt, in, pl.pos, table, sh);
+        else
+          segment<I8, V, TURN, true>(a, t, cnt, page, first, first / bt, in, pl.pos, table, sh);
+      }
+      t += cnt;
+      if (more) {
+        pl.i += cnt;
+        pl.pos += cnt;
+        continue;
+      }
+    } else {  // the rest of a malformed request (or of the table) is skipped
+      if (pl.i < 0 || cnt <= 0) return;
+      t += cnt;
     }
-    const int in = pl.pos % bt;
-    const int cnt = min(min(bt - in, pl.n - pl.i), total - t);
-    if (pl.i == 0 || in == 0) {
-      const int first = pl.pos % a.page_size - in;  // the block's first slot
-      __syncthreads();  // the last segment's shared values have been read
-      segment<I8, V, TURN>(a, t, cnt, pl.page, first, first / bt, in, pl.pos, table, sh);
-    }
-    t += cnt;
+    if (t >= t1) return;
+    pl = find_place(a, t, lane);
   }
 }
 
-template <bool I8, int TURN>
+template <bool I8, int TURN, bool LONG>
 __global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(const __grid_constant__ AppendArgs a) {
   extern __shared__ float4 table[];
   __shared__ BlockShared sh;
@@ -382,8 +408,8 @@ __global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(cons
   const int b = blockIdx.x, stripe = b / a.stripe, window = (stripe >> 1) * a.stripe + b % a.stripe;
   if (b < a.num_kv_blocks) {
     if (window >= a.num_windows) return;
-    if (stripe & 1) window_segments<I8, true, kCopy>(a, window, table, sh);
-    else window_segments<I8, false, TURN>(a, window, table, sh);
+    if (stripe & 1) window_segments<I8, true, kCopy, LONG>(a, window, table, sh);
+    else window_segments<I8, false, TURN, LONG>(a, window, table, sh);
   } else {
     const int t0 = (b - a.num_kv_blocks) * a.per_q_block;
     rows_pass<MODE_NONE, 32 * kBlockWarps>(a, t0, min(a.per_q_block, a.num_rows - t0), table);
@@ -392,13 +418,18 @@ __global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(cons
 
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+template <bool I8, bool LONG>
+int launch_turn(const AppendArgs& a, int blocks, int smem, cudaStream_t s) {
+  constexpr int threads = 32 * kBlockWarps;
+  if (a.f.dim == 0) append_blocks_kernel<I8, kCopy, LONG><<<blocks, threads, smem, s>>>(a);
+  else if (a.f.halves) append_blocks_kernel<I8, kHalves, LONG><<<blocks, threads, smem, s>>>(a);
+  else append_blocks_kernel<I8, kInterleaved, LONG><<<blocks, threads, smem, s>>>(a);
+  return (int)cudaGetLastError();
+}
 template <bool I8>
 int launch_blocks(const AppendArgs& a, int blocks, int smem, cudaStream_t s) {
-  constexpr int threads = 32 * kBlockWarps;
-  if (a.f.dim == 0) append_blocks_kernel<I8, kCopy><<<blocks, threads, smem, s>>>(a);
-  else if (a.f.halves) append_blocks_kernel<I8, kHalves><<<blocks, threads, smem, s>>>(a);
-  else append_blocks_kernel<I8, kInterleaved><<<blocks, threads, smem, s>>>(a);
-  return (int)cudaGetLastError();
+  return a.block_tokens > kTableTokens ? launch_turn<I8, true>(a, blocks, smem, s)
+                                       : launch_turn<I8, false>(a, blocks, smem, s);
 }
 
 }  // namespace
@@ -460,9 +491,10 @@ int launch_kv_append(const skv_append_params& p, cudaStream_t s) {
     else append_rows_kernel<MODE_E4M3><<<blocks, kRowThreads, smem, s>>>(a);
     return (int)cudaGetLastError();
   }
-  // windows of one row while there are few, then up to a block's tokens (one or two segments each)
-  a.per_block = (int)std::min<int64_t>(std::min(p.block_tokens, kTableTokens),
-                                       std::max<int64_t>(1, p.num_rows / (sms * 4)));
+  // windows of one row while there are few, then three an SM for each of K and V: two blocks are
+  // resident, and the third evens out what segments of unlike lengths leave (one, two, three, four an
+  // SM: 50.8, 49.0, 43.2, 45.2 us at the size that the top names)
+  a.per_block = (int)std::max<int64_t>(1, p.num_rows / (sms * 3));
   a.num_windows = cdiv(p.num_rows, a.per_block);
   a.per_q_block = 1;
   a.stripe = (int)std::min<int64_t>(sms, a.num_windows);

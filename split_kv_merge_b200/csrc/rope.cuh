@@ -96,13 +96,20 @@ __device__ __forceinline__ void fill_table(float4* table, const int32_t* pos, in
   const int half = dim / 2, items = dim / 16;
   if (half == 0) return;  // nothing turns
   float2* t2 = reinterpret_cast<float2*>(table);
-  for (int x = tid; x < n * half; x += threads) {
-    const int tok = x / half, p = x - tok * half;
+  int tok = tid / half, p = tid - tok * half;  // then on by `threads` pairs, without dividing again
+  const int tok_step = threads / half, p_step = threads - tok_step * half;
+  while (tok < n) {
     // halves: pair p is number p % 8 of item p / 8; interleaved: of chunk p / 4, which is the item's first or
     // second one
     const int second = !halves && p >= 4 * items, i = halves ? p >> 3 : (p >> 2) - (second ? items : 0);
     const int j = halves ? (p & 7) >> 1 : 2 * second + ((p & 3) >> 1);
     t2[tok * half + (j * items + i) * 2 + (p & 1)] = cos_sin(pos[tok], turns[p], mscale);
+    tok += tok_step;
+    p += p_step;
+    if (p >= half) {
+      p -= half;
+      ++tok;
+    }
   }
 }
 

@@ -193,12 +193,66 @@ skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int3
   }
   // a span longer than 1.5 shares of the whole work is cut along the keys (pieces of >= 8 tiles)
   const int64_t chunk = std::max<int64_t>(8, (total + ctas - 1) / ctas);
+  std::vector<int32_t> cuts(spans.size());
+  bool whole = true;
+  for (size_t i = 0; i < spans.size(); ++i) {
+    cuts[i] = 2 * (int64_t)spans[i].tiles > 3 * chunk ? (int32_t)((spans[i].tiles + chunk - 1) / chunk) : 1;
+    whole = whole && cuts[i] == 1;
+  }
+  // A few items per CTA leave some CTAs one item short.  Where that costs a twentieth, the spans of as many
+  // of the shortest items as make no full round are cut too, if the longest CTA's share and the pass that
+  // joins the partials (about 3 us and their bytes twice, at 1 us for half an item's tile) then end sooner.
+  // 4096 query tokens over 16384 keys, 32/8 heads: 441 -> 395 tiles for the longest CTA, 951 -> 886-921 us.
+  const int64_t whole_items = (int64_t)spans.size() * head_items;
+  if (whole && whole_items > ctas && whole_items < 8LL * ctas) {
+    std::vector<int32_t> by_len(spans.size());
+    for (size_t i = 0; i < by_len.size(); ++i) by_len[i] = (int32_t)i;
+    std::stable_sort(by_len.begin(), by_len.end(), [&](int32_t x, int32_t y) { return spans[x].tiles > spans[y].tiles; });
+    const auto ends_at = [&](size_t cut, int32_t pieces) {  // the last `cut` of by_len in `pieces` each
+      std::vector<int64_t> costs;
+      int64_t rows = 0;
+      for (size_t k = 0; k < by_len.size(); ++k) {
+        const Span& s = spans[by_len[k]];
+        const int32_t n = k + cut < by_len.size() ? 1 : pieces;
+        if (n > 1) rows += (int64_t)s.n * n;
+        for (int32_t j = 0; j < n; ++j) {
+          const int64_t t = (int64_t)s.tiles * (j + 1) / n - (int64_t)s.tiles * j / n;
+          costs.insert(costs.end(), head_items, t * (heads || s.n > kPromptTile ? 2 : 1) + 3);
+        }
+      }
+      std::stable_sort(costs.begin(), costs.end(), std::greater<int64_t>());
+      std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;
+      for (int32_t c = 0; c < ctas; ++c) load.push(0);
+      int64_t most = 0;
+      for (int64_t c : costs) {
+        const int64_t l = load.top() + c;
+        load.pop();
+        load.push(l);
+        most = std::max(most, l);
+      }
+      return most + (rows > 0 ? 3 + rows * num_qo_heads * head_dim * 8 / 6000000 : 0);
+    };
+    int64_t best = ends_at(0, 1), best_cut = 0, best_pieces = 1;
+    if (best * 20 > 21 * (2 * total + 3 * whole_items) / ctas) {
+      const int64_t round = (whole_items % ctas + head_items - 1) / head_items;
+      for (int64_t cut : {round, round + 1}) {
+        cut = std::min<int64_t>(cut, (int64_t)spans.size());
+        for (int32_t pieces : {2, 3, 4, 6}) {
+          if (cut < 1 || spans[by_len.back()].tiles < 8 * pieces) break;
+          const int64_t e = ends_at((size_t)cut, pieces);
+          if (e < best) best = e, best_cut = cut, best_pieces = pieces;
+        }
+      }
+      for (int64_t k = 0; k < best_cut; ++k) cuts[by_len[by_len.size() - 1 - k]] = (int32_t)best_pieces;
+    }
+  }
   std::vector<PromptItem> items;
   std::vector<MergeItem> merges;
   int64_t part_rows = 0;
-  for (const Span& s : spans) {
+  for (size_t si = 0; si < spans.size(); ++si) {
+    const Span& s = spans[si];
     const int64_t n = (int64_t)qo_indptr_h[s.r + 1] - qo_indptr_h[s.r], len = (int64_t)kv[s.r + 1] - kv[s.r];
-    const int32_t pieces = 2 * (int64_t)s.tiles > 3 * chunk ? (int32_t)((s.tiles + chunk - 1) / chunk) : 1;
+    const int32_t pieces = cuts[si];
     info->max_splits = std::max(info->max_splits, pieces);
     info->total_splits += pieces;
     if (part_rows + (int64_t)s.n * pieces > INT32_MAX) return SKV_ERR_UNSUPPORTED;

@@ -18,11 +18,19 @@
 // one issuer for both sides was busy 4130 cycles per pair of tiles (clock stamps of one CTA).  The two
 // issue in strict turns: left to themselves A and B fall into step, both in the softmax and then both
 // at the tensor cores (1214 us against 956 us on 4096 query tokens over 16384 keys, 32/8 heads).
+// What is left is the chain of one side: 2100 cycles of softmax, its weights' way to the issuer, 1024 of
+// MMAs, their scores' way back: 3800 for a pair of tiles, 2048 of them the tensor cores'.  Scores in two
+// buffers of 64 keys, which break that chain, measured slower (1072 us): a 128 x 64 x 16 product of two
+// shared-memory operands takes 59 cycles, the one of 128 x 128 x 16 only 64.  Weights handed over in
+// halves with the maximum taken beside the exponentials: 1005 us.
 // The running maximum is raised only when a score passes it by 2^8, so O is rarely rescaled.
 //
 // Persistent: the planner hands every CTA a list of items (a pair of query tiles and a range of
-// key tiles), longest first onto the least loaded.  Items of few rows over many keys are cut along
-// the keys into fp32 partials that the merge pass joins.  Roles: warps 0-3 softmax of A, 4-7 of B,
+// key tiles), longest first onto the least loaded.  Items of few rows over many keys, and a few of
+// those that would make no full round, are cut along the keys into fp32 partials that the merge pass
+// joins.  An item's end costs about 6000 cycles (the last P V, its results, the next item's first
+// scores): its code runs once in a while and is kept short, and results leave as whole lines (16
+// sequences of 64 .. 2048 tokens: 218 -> 203 us).  Roles: warps 0-3 softmax of A, 4-7 of B,
 // warp 8 TMA (ring of K and V tiles in the order of use), warps 9 and 10 the MMAs of A and of B.
 // All waits are bounded.
 #include <cudaTypedefs.h>
@@ -132,6 +140,26 @@ __device__ __forceinline__ void weights(const float (&s)[kTile], uint64_t sc2, u
   }
 }
 
+// 32 words of a row in every lane become whole lines: an 8 x 8 transposition of 16-byte chunks
+// among 8 lanes, after which lane i of them holds chunk i of their rows 0..7 (chunk c of `u`: row c).
+__device__ __forceinline__ void transpose8(uint32_t (&u)[32], int lane) {
+#pragma unroll
+  for (int b = 1; b < 8; b <<= 1) {
+    const bool hi = lane & b;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c & b) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &lo_w = u[c * 4 + e], &hi_w = u[(c + b) * 4 + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? lo_w : hi_w, b);
+        if (hi) lo_w = got;
+        else hi_w = got;
+      }
+    }
+  }
+}
+
 // The two query tiles of an item, and the key tiles [0, tiles) of its range that each one needs.
 struct Side {
   int q0, n, head, limit, tiles;
@@ -157,6 +185,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = tc::smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i_begin = a.cta_indptr[blockIdx.x], i_end = a.cta_indptr[blockIdx.x + 1];
   tc::grid_launch_dependents();  // the merge pass may be scheduled; it waits for this grid
 
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + S::misc);
@@ -192,7 +221,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t tm_s[2] = {tmem, tmem + kTile}, tm_o[2] = {tmem + 2 * kTile, tmem + 3 * kTile};
-  const int i_begin = a.cta_indptr[blockIdx.x], i_end = a.cta_indptr[blockIdx.x + 1];
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -344,8 +372,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
     int s_it = 0, o_it = 0;
     int v_seq = 0;  // ring loads of the items before this one
     bool ok = true;
+    PromptItem next = a.items[i_begin];  // the planner leaves no CTA without an item
     for (int i = i_begin; i < i_end; ++i) {
-      const PromptItem w = a.items[i];
+      const PromptItem w = next;
       const Side s_me = side_of(w, x);
       const int tiles = s_me.tiles, all_tiles = max(tiles, side_of(w, 1 - x).tiles);
       // l: sum of the exact weights, the divisor of O too: P V multiplies them rounded to bf16, each
@@ -392,7 +421,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           l *= al;
           m = mn;
           if (j > 0) {  // a full S(j) means P V(j - 1) is done
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               float v[16];
               tc::tmem_ld_x16(to + c, v);
@@ -439,47 +468,67 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         ++o_it;
         tc::tc_fence_after();
       }
-      const bool live = r < s_me.n && s_me.q0 + r < a.total_q;
+      next = a.items[min(i + 1, i_end - 1)];  // on its way while the results are stored
       const bool some = l > 0.f || l != l;
       const float inv = some ? 1.f / l : 0.f;
-      OutT* oo = nullptr;
-      float* op = nullptr;
-      if (live) {
-        const float lse = some ? (m + log2f(l)) * kLn2 : -INFINITY;
-        const int64_t row = s_me.q0 + r;
-        if (w.part_row < 0) {
-          oo = reinterpret_cast<OutT*>(a.o) + (row * a.hq + s_me.head) * D;
-          if (a.lse != nullptr) a.lse[row * a.hq + s_me.head] = lse;
-        } else {
-          const int64_t part = (int64_t)w.part_row + (int64_t)(row - w.q0a) * w.part_stride;
-          op = a.o_part + (part * a.hq + s_me.head) * D;
-          a.lse_part[part * a.hq + s_me.head] = lse;
-        }
-      }
+      const int rows = min(s_me.n, a.total_q - s_me.q0);
+      const bool part = w.part_row >= 0;
+      // this tile's first row, and rows a token apart
+      const int64_t row0 = part ? (int64_t)w.part_row + (int64_t)(s_me.q0 - w.q0a) * w.part_stride : (int64_t)s_me.q0;
+      const int64_t step = part ? w.part_stride : 1;
+      float* const lse = part ? a.lse_part : a.lse;
+      if (r < rows && lse != nullptr)
+        lse[(row0 + r * step) * a.hq + s_me.head] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+      // 128 bytes of a row at a time, turned so that eight lanes write them
+      auto store = [&](uint32_t (&u)[32], void* base, int64_t row_bytes, int byte) {
+        transpose8(u, lane);
+        uint8_t* dst = static_cast<uint8_t*>(base) + byte + (lane & 7) * 16;
 #pragma unroll
-      for (int c = 0; c < D; c += 16) {
-        float v[16];
-        if (tiles > 0) {  // the whole warp loads; live rows store
+        for (int c = 0; c < 8; ++c) {
+          const int row = quarter * 32 + (lane & 24) + c;
+          if (row < rows)
+            *reinterpret_cast<uint4*>(dst + row * row_bytes) = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+        }
+      };
+      auto load_o = [&](int c, float (&v)[16]) {  // the whole warp loads
+        if (tiles > 0) {
           tc::tmem_ld_x16(to + c, v);
           tc::tmem_wait_ld();
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = some ? v[e] * inv : 0.f;
-        if (op != nullptr || (oo != nullptr && sizeof(OutT) == 4)) {
-          float* dst = (op != nullptr ? op : reinterpret_cast<float*>(oo)) + c;
+      };
+      const int64_t out0 = (row0 * a.hq + s_me.head) * D;
+      if (part || sizeof(OutT) == 4) {
+        float* base = (part ? a.o_part : reinterpret_cast<float*>(a.o)) + out0;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t u[32];
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-        } else if (oo != nullptr) {
-          uint32_t u[8];
+          for (int k = 0; k < 32; k += 16) {
+            float v[16];
+            load_o(c + k, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-            u[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            for (int e = 0; e < 16; ++e) u[k + e] = __float_as_uint(v[e]);
           }
-          uint4* dst = reinterpret_cast<uint4*>(oo + c);
-          dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
-          dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+          store(u, base, step * a.hq * D * 4, c * 4);
+        }
+      } else {
+        OutT* base = reinterpret_cast<OutT*>(a.o) + out0;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t u[32];
+#pragma unroll
+          for (int k = 0; k < 64; k += 16) {
+            float v[16];
+            load_o(c + k, v);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[e], v[e + 1]);
+              u[(k + e) >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+          }
+          store(u, base, (int64_t)a.hq * D * 2, c * 2);
         }
       }
       tc::tc_fence_before();  // O has been read before the next item's first P is announced

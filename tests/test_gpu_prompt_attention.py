@@ -91,6 +91,16 @@ def test_cut_along_the_keys(hq, hk):
         assert torch.equal(ob, o.to(torch.bfloat16)) and torch.equal(lb, lse)
 
 
+@pytest.mark.parametrize("hq,hk,sms", [(4, 2, 20), (3, 1, 16)])
+def test_uneven_rounds_are_cut(hq, hk, sms):
+    """More items than CTAs, but no full round of them: the shortest are cut, the others stay whole."""
+    c = Case(9, [1500], [4100], hq, hk, 128)
+    plan = skv.plan_prompt(c.qo, c.kv, hq, hk, 128, True, sms)
+    assert 0 < plan.info.num_merge_rows < 1500 and plan.info.num_ctas <= sms
+    o, lse, _ = c.run(True, plan=plan)
+    c.check(o, lse, True)
+
+
 def test_other_sequences_never_reach_a_result():
     """NaN and infinite keys and values of one sequence stay in it, wherever its neighbours' tiles end."""
     for hq, hk in ((4, 2), (3, 3)):

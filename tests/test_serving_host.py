@@ -283,21 +283,17 @@ def test_plan_prompt_refusals(args, kw, code):
     assert _plan_prompt(*args, **kw)[0] == code
 
 
-@pytest.mark.parametrize("hq,hk", [(4, 2), (3, 1), (5, 5), (8, 1)])
-@pytest.mark.parametrize("causal", [0, 1])
-@pytest.mark.parametrize("q_lens,kv_lens", [([1, 300, 0, 128, 129], None), ([5, 64, 700], [4000, 20, 900]),
-                                            ([100], [30000]), ([7, 3], [0, 2])])
-def test_plan_prompt_covers_every_pair_once(hq, hk, causal, q_lens, kv_lens):
+def _covers(hq, hk, causal, q_lens, kv_lens, sms=148):
     """Each (query token, head) meets each key tile that it sees in exactly one item; its partial rows and merge
     items agree; the CTAs' lists hold every item once."""
     kv_lens = q_lens if kv_lens is None else kv_lens
     qo, kv = (np.concatenate([[0], np.cumsum(x)]) for x in (q_lens, kv_lens))
-    code, plan, info = _plan_prompt(qo, kv, hq, hk, 64, causal)
+    code, plan, info = _plan_prompt(qo, kv, hq, hk, 64, causal, sms)
     assert code == skv.OK and info.kernel == 6
     items = plan[:16 * info.num_work].reshape(-1, 16)
     merges = plan[16 * info.num_work:16 * info.num_work + 4 * info.num_merge_rows].reshape(-1, 4)
     lists = plan[info.cta_offset:info.cta_offset + info.num_ctas + 1]
-    assert lists[0] == 0 and lists[-1] == info.num_work and np.all(np.diff(lists) >= 1) and info.num_ctas <= 148
+    assert lists[0] == 0 and lists[-1] == info.num_work and np.all(np.diff(lists) >= 1) and info.num_ctas <= sms
     merged = {int(m[0]): (int(m[1]), int(m[2])) for m in merges}
     tiles = -(-max(max(kv_lens), 1) // 128)
     met = np.zeros((int(qo[-1]), hq, tiles), int)
@@ -329,6 +325,27 @@ def test_plan_prompt_covers_every_pair_once(hq, hk, causal, q_lens, kv_lens):
     if info.num_partial_rows:
         assert np.all(written == 1)
         assert sum(c for _, c in merged.values()) == info.num_partial_rows
+    return items, lists
+
+
+@pytest.mark.parametrize("hq,hk", [(4, 2), (3, 1), (5, 5), (8, 1)])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 300, 0, 128, 129], None), ([5, 64, 700], [4000, 20, 900]),
+                                            ([100], [30000]), ([7, 3], [0, 2])])
+def test_plan_prompt_covers_every_pair_once(hq, hk, causal, q_lens, kv_lens):
+    _covers(hq, hk, causal, q_lens, kv_lens)
+
+
+@pytest.mark.parametrize("hq,hk,q_lens,kv_lens,sms", [(4, 2, [1500], [3600], 20), (3, 1, [1500], [5100], 16),
+                                                      (32, 8, [1024], [4000], 100), (2, 1, [900, 700], [4000, 3000], 12)])
+def test_plan_prompt_evens_out_uneven_rounds(hq, hk, q_lens, kv_lens, sms):
+    """Where whole items leave CTAs one item short, some are cut along the keys, and the longest list shrinks."""
+    items, lists = _covers(hq, hk, 1, q_lens, kv_lens, sms)
+    whole = len({(int(w[0]), int(w[4])) for w in items})
+    assert sms < whole < len(items)
+    tiles = items[:, 11] - items[:, 10]
+    load = np.array([tiles[a:b].sum() for a, b in zip(lists[:-1], lists[1:])])
+    assert load.max() <= 1.15 * tiles.sum() / sms
 
 
 def _prompt_params(**kw):

@@ -361,12 +361,13 @@ def plan_prompt(qo_indptr, kv_indptr, num_qo_heads: int, num_kv_heads: int, head
         raise ValueError("qo_indptr and kv_indptr must name the same sequences")
     info = PlanInfo()
     args = (len(qo) - 1, _ptr_i32(qo), _ptr_i32(ki), num_qo_heads, num_kv_heads, head_dim, int(causal), num_sms)
-    code = _plan_prompt(*args, None, 0, ctypes.byref(info))
-    if code not in (OK, ERR_WORKSPACE):
-        _check(code, "skv_plan_prompt")
-    words = np.zeros(max(1, info.plan_words), dtype=np.int32)
-    _check(_plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info)), "skv_plan_prompt")
-    return Plan(words[: info.plan_words] if info.plan_words else words[:0], info)
+    words = np.empty(1 << 14, dtype=np.int32)  # most plans fit, and are made once
+    code = _plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info))
+    if code == ERR_WORKSPACE:
+        words = np.empty(info.plan_words, dtype=np.int32)
+        code = _plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info))
+    _check(code, "skv_plan_prompt")
+    return Plan(words[: info.plan_words].copy(), info)
 
 
 # ----------------------------------------------------------------------------- launches

@@ -210,6 +210,7 @@ skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int3
     std::stable_sort(by_len.begin(), by_len.end(), [&](int32_t x, int32_t y) { return spans[x].tiles > spans[y].tiles; });
     const auto ends_at = [&](size_t cut, int32_t pieces) {  // the last `cut` of by_len in `pieces` each
       std::vector<int64_t> costs;
+      costs.reserve((by_len.size() + cut * pieces) * head_items);
       int64_t rows = 0;
       for (size_t k = 0; k < by_len.size(); ++k) {
         const Span& s = spans[by_len[k]];
@@ -220,7 +221,7 @@ skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int3
           costs.insert(costs.end(), head_items, t * (heads || s.n > kPromptTile ? 2 : 1) + 3);
         }
       }
-      std::stable_sort(costs.begin(), costs.end(), std::greater<int64_t>());
+      std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
       std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;
       for (int32_t c = 0; c < ctas; ++c) load.push(0);
       int64_t most = 0;
@@ -234,14 +235,11 @@ skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int3
     };
     int64_t best = ends_at(0, 1), best_cut = 0, best_pieces = 1;
     if (best * 20 > 21 * (2 * total + 3 * whole_items) / ctas) {
-      const int64_t round = (whole_items % ctas + head_items - 1) / head_items;
-      for (int64_t cut : {round, round + 1}) {
-        cut = std::min<int64_t>(cut, (int64_t)spans.size());
-        for (int32_t pieces : {2, 3, 4, 6}) {
-          if (cut < 1 || spans[by_len.back()].tiles < 8 * pieces) break;
-          const int64_t e = ends_at((size_t)cut, pieces);
-          if (e < best) best = e, best_cut = cut, best_pieces = pieces;
-        }
+      const int64_t cut = (whole_items % ctas + head_items - 1) / head_items;
+      for (int32_t pieces : {2, 3, 4, 6}) {
+        if (cut < 1 || spans[by_len.back()].tiles < 8 * pieces) break;
+        const int64_t e = ends_at((size_t)cut, pieces);
+        if (e < best) best = e, best_cut = cut, best_pieces = pieces;
       }
       for (int64_t k = 0; k < best_cut; ++k) cuts[by_len[by_len.size() - 1 - k]] = (int32_t)best_pieces;
     }

@@ -433,6 +433,8 @@ SKV_API skv_status skv_mla_splice(const skv_splice_params* p, const skv_splice_c
  *   t <= L - n + i; a token that sees none gets O = 0, LSE = -inf.  Made for a few query tokens
  *   per request (decode, drafted tokens); every tile of 8 or 16 query rows (tokens x group)
  *   streams the request's keys again.
+ *   Scales are >= 0; below 2^-126 they count as 0, and |q| * sm_scale * k_scale * 2^24 and
+ *   v_scale * 2^24 must be finite (int8).  A request has at most 2^30 tokens.
  *   Slots past a request's length may hold anything, NaN codes and scales included.  A key that
  *   some query token of its request sees must have finite K, V and scales: where it is masked
  *   for another token of the request its weight is 0, and 0 x NaN is not 0.
@@ -472,7 +474,8 @@ SKV_API skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* p, c
  *   own sequence sees must have finite K and V (where it is masked for another token its weight is
  *   0, and 0 x NaN is not 0).
  *   `num_sms` (0: the current device's) is what the plan balances over; sequences with few query
- *   tokens over many keys are cut along the keys, their partials go to o_part / lse_part
+ *   tokens over many keys, and a few others where whole ones would leave SMs idle, are cut along the
+ *   keys, their partials go to o_part / lse_part
  *   ([num_partial_rows, Hq, D] and [num_partial_rows, Hq]) and are merged on the same stream.
  * ----------------------------------------------------------------------------------------- */
 SKV_API skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,

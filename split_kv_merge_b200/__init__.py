@@ -275,6 +275,7 @@ class Plan:
     words: np.ndarray
     info: PlanInfo
     device: Optional[object] = None
+    made_for: Optional[tuple] = None  # what the serving calls compare a kept plan with
 
     def to(self, device, non_blocking: bool = False):
         import torch
@@ -347,9 +348,11 @@ def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, nu
     """Host planner (skv_plan_paged_scaled) for attention over an 8-bit cache with block scales."""
     qo, ki, la = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_last_page_len)
     b = len(ki) - 1
-    return _plan(_plan_scaled, lambda pol: (b, _ptr_i32(qo), _ptr_i32(ki), _ptr_i32(la), page_size, num_qo_heads,
+    plan = _plan(_plan_scaled, lambda pol: (b, _ptr_i32(qo), _ptr_i32(ki), _ptr_i32(la), page_size, num_qo_heads,
                                             num_kv_heads, head_dim, int(causal), pol, param),
                  policy, split_page_start, "skv_plan_paged_scaled")
+    plan.made_for = (b, int(qo[-1]), int(ki[-1]), page_size, num_qo_heads, num_kv_heads, head_dim, bool(causal))
+    return plan
 
 
 def plan_prompt(qo_indptr, kv_indptr, num_qo_heads: int, num_kv_heads: int, head_dim: int, causal: bool = True,
@@ -367,7 +370,9 @@ def plan_prompt(qo_indptr, kv_indptr, num_qo_heads: int, num_kv_heads: int, head
         words = np.empty(info.plan_words, dtype=np.int32)
         code = _plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info))
     _check(code, "skv_plan_prompt")
-    return Plan(words[: info.plan_words].copy(), info)
+    total_kv = int(qo[-1] if ki is None else ki[-1])
+    return Plan(words[: info.plan_words].copy(), info,
+                made_for=(len(qo) - 1, int(qo[-1]), total_kv, num_qo_heads, num_kv_heads, head_dim, bool(causal)))
 
 
 # ----------------------------------------------------------------------------- launches

@@ -601,7 +601,7 @@ skv_status skv_plan_paged_scaled(int32_t batch, const int32_t* qo_indptr_h, cons
     const int32_t r = work[i].r;
     const int64_t seen = kv_len[r] - req[r].q_len + (work[i].q_start - req[r].q_start) + 1;
     work[i].split = causal ? (int32_t)std::max<int64_t>(seen, -(1 << 30)) : 1 << 30;
-    if (!causal && kv_len[r] > (1 << 30)) return SKV_ERR_UNSUPPORTED;
+    if (kv_len[r] > (1 << 30)) return SKV_ERR_UNSUPPORTED;  // token indices and limits stay in 32 bits
   }
   return SKV_OK;
 } catch (...) {

@@ -41,11 +41,12 @@ skv_status check_rows(const void* base, const int64_t* stride, int64_t size) {
   return SKV_OK;
 }
 
-// Output rows, which may also be the input with the same strides.
+// Output rows, which may also be the input with the same strides; each has a place of its own.
 skv_status check_out_rows(const void* out, const int64_t* out_stride, const void* in, const int64_t* in_stride,
-                          int64_t size) {
+                          int64_t size, int64_t tokens, int64_t heads) {
   const skv_status st = check_rows(out, out_stride, size);
   if (st != SKV_OK) return st;
+  if ((tokens > 1 && out_stride[0] == 0) || (heads > 1 && out_stride[1] == 0)) return SKV_ERR_INVALID;
   if (out == in && (out_stride[0] != in_stride[0] || out_stride[1] != in_stride[1])) return SKV_ERR_INVALID;
   return SKV_OK;
 }
@@ -105,12 +106,14 @@ skv_status skv_rope_apply(const skv_rope_params* p, skv_stream_t stream) {
   const int64_t size = p->dtype == SKV_F32 ? 4 : 2;
   if (p->num_q_heads > 0) {
     st = check_rows(p->q, p->q_stride, size);
-    if (st == SKV_OK) st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, size);
+    if (st == SKV_OK)
+      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, size, p->num_tokens, p->num_q_heads);
     if (st != SKV_OK) return st;
   }
   if (p->num_k_heads > 0) {
     st = check_rows(p->k, p->k_stride, size);
-    if (st == SKV_OK) st = check_out_rows(p->k_out, p->k_out_stride, p->k, p->k_stride, size);
+    if (st == SKV_OK)
+      st = check_out_rows(p->k_out, p->k_out_stride, p->k, p->k_stride, size, p->num_tokens, p->num_k_heads);
     if (st != SKV_OK) return st;
   }
   if (p->rope.dim > 0 && p->positions == nullptr) return SKV_ERR_INVALID;
@@ -133,7 +136,8 @@ skv_status skv_paged_kv_append(const skv_append_params* p, skv_stream_t stream) 
     if (p->page_size % p->block_tokens != 0) return SKV_ERR_INVALID;
   } else if (p->kv_dtype == SKV_I8) {
     return SKV_ERR_UNSUPPORTED;
-  } else if (p->kv_dtype == SKV_E4M3 && !(p->kv_scale > 0.f && std::isfinite(p->kv_scale) && std::isfinite(1.f / p->kv_scale))) {
+  } else if (p->kv_dtype == SKV_E4M3 &&
+             !(p->kv_scale > 0.f && std::isfinite(p->kv_scale) && std::isfinite(1.f / p->kv_scale))) {
     return SKV_ERR_INVALID;
   }
   if (p->num_rows == 0 || p->batch == 0) return SKV_OK;
@@ -147,11 +151,17 @@ skv_status skv_paged_kv_append(const skv_append_params* p, skv_stream_t stream) 
     if (p->k_stride[i] < 0 || p->v_stride[i] < 0) return SKV_ERR_INVALID;
     if (p->k_stride[i] * size % 16 != 0 || p->v_stride[i] * size % 16 != 0) return SKV_ERR_ALIGNMENT;
     if (scaled && (p->k_scale_stride[i] < 0 || p->v_scale_stride[i] < 0)) return SKV_ERR_INVALID;
+    // what is written has a place of its own
+    const int32_t entries[3] = {p->num_pages, p->page_size, p->num_kv_heads};
+    if (entries[i] > 1 && (p->k_stride[i] == 0 || p->v_stride[i] == 0)) return SKV_ERR_INVALID;
+    const int32_t scales[3] = {p->num_pages, scaled ? p->page_size / p->block_tokens : 0, p->num_kv_heads};
+    if (scaled && scales[i] > 1 && (p->k_scale_stride[i] == 0 || p->v_scale_stride[i] == 0)) return SKV_ERR_INVALID;
   }
   if (!aligned16(p->k_cache) || !aligned16(p->v_cache)) return SKV_ERR_ALIGNMENT;
   if (p->num_q_heads > 0) {
     st = check_rows(p->q, p->q_stride, 2);
-    if (st == SKV_OK) st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, 2);
+    if (st == SKV_OK)
+      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, 2, p->num_rows, p->num_q_heads);
     if (st != SKV_OK) return st;
   }
   return cuda_status(launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream)));
@@ -207,7 +217,8 @@ skv_status skv_plan_prompt(int32_t batch, const int32_t* qo_indptr_h, const int3
   if (whole && whole_items > ctas && whole_items < 8LL * ctas) {
     std::vector<int32_t> by_len(spans.size());
     for (size_t i = 0; i < by_len.size(); ++i) by_len[i] = (int32_t)i;
-    std::stable_sort(by_len.begin(), by_len.end(), [&](int32_t x, int32_t y) { return spans[x].tiles > spans[y].tiles; });
+    std::stable_sort(by_len.begin(), by_len.end(),
+                     [&](int32_t x, int32_t y) { return spans[x].tiles > spans[y].tiles; });
     const auto ends_at = [&](size_t cut, int32_t pieces) {  // the last `cut` of by_len in `pieces` each
       std::vector<int64_t> costs;
       costs.reserve((by_len.size() + cut * pieces) * head_items);

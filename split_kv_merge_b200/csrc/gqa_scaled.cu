@@ -547,7 +547,7 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           }
         }
         if constexpr (!TMA) vref = quad_max(vref);
-        const float rv = vref > 0.f ? 1.f / vref : 0.f;
+        const float rv = vref >= 1.17549435e-38f ? 1.f / vref : 0.f;  // subnormal scales count as 0
         bool raise = false;
 #pragma unroll
         for (int r = 0; r < kRowSets; ++r) {

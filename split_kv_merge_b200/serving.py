@@ -124,6 +124,11 @@ def _o_code(o_dtype) -> int:
     return code
 
 
+def _same(plan: Plan, made_for: tuple):
+    if plan.made_for is not None and plan.made_for != made_for:
+        _bad(f"the plan was made for other requests: {plan.made_for}, not {made_for}")
+
+
 def _dev_i32(a, like):
     import torch
     return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype=np.int32))).to(like.device)
@@ -138,8 +143,8 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
     bf16, caches [num_pages, P, Hk, D] float8_e4m3fn or int8, ``k_scale`` / ``v_scale`` float32
     [num_pages, P / block, Hk], as ``paged_kv_append`` writes them.  ``causal``: a request's query tokens are
     its last positions and each sees keys up to its own.  Host page-table shape arrays (``*_h``) feed
-    the planner; ``plan`` (``plan_paged_scaled`` with the same ``causal``) and device copies ``kv_indptr`` /
-    ``kv_last_page_len`` may be kept over the layers of a step.
+    the planner; ``plan`` (``plan_paged_scaled`` of the same lengths, heads and ``causal``) and device copies
+    ``kv_indptr`` / ``kv_last_page_len`` may be kept over the layers of a step.
     Returns (o, lse, extras) with extras = {"plan", "workspace"} (the split partials' buffer)."""
     if stream is not None:
         with _on_stream(stream, q):
@@ -154,6 +159,9 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
     if plan is None:
         plan = plan_paged_scaled(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, k_cache.shape[1], q.shape[1],
                                  k_cache.shape[2], q.shape[2], causal, policy, param, split_page_start)
+    else:
+        _same(plan, (len(qo_indptr_h) - 1, int(qo_indptr_h[-1]), int(kv_indptr_h[-1]), k_cache.shape[1], q.shape[1],
+                     k_cache.shape[2], q.shape[2], bool(causal)))
     if plan.device is None:
         plan.to(q.device)
     if kv_indptr is None:
@@ -173,8 +181,8 @@ def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = T
     """Attention over packed prompts (skv_prompt_attn_fwd): q [total_q, Hq, D], k, v [total_kv, Hk, D] bf16, any
     token / head strides; sequence r has query rows qo_indptr_h[r] .. and key rows kv_indptr_h[r] ..
     (default: the same rows).  ``causal``: its query tokens are its last positions.  ``plan``
-    (``plan_prompt`` with the same ``causal``) may be kept over the layers of a step.  Rows of outputs given as
-    ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
+    (``plan_prompt`` of the same lengths, heads and ``causal``) may be kept over the layers of a step.  Rows of
+    outputs given as ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
     Returns (o, lse, extras) with extras = {"plan", "workspace"} (the partials' buffer)."""
     if stream is not None:
         with _on_stream(stream, q):
@@ -186,6 +194,10 @@ def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = T
         _bad("q is [total_q, Hq, D], k and v are [total_kv, Hk, D] with the rows qo_indptr and kv_indptr name")
     if plan is None:
         plan = plan_prompt(qo_indptr_h, kv_indptr_h, q.shape[1], k.shape[1], q.shape[2], causal)
+    else:
+        ki = qo_indptr_h if kv_indptr_h is None else kv_indptr_h
+        _same(plan, (len(qo_indptr_h) - 1, int(qo_indptr_h[-1]), int(ki[-1]), q.shape[1], k.shape[1], q.shape[2],
+                     bool(causal)))
     if plan.device is None:
         plan.to(q.device)
     o, lse, ws = ext.prompt_attention(q, k, v, plan.device, ctypes.addressof(plan.info), sm_scale, _o_code(o_dtype),

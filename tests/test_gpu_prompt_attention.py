@@ -194,6 +194,19 @@ def test_no_rows_and_no_keys():
         assert bool(torch.all(o == 0)) and bool(torch.all(torch.isneginf(lse)))
 
 
+def test_rows_past_32_bit_offsets():
+    """Tokens 8.4 million values apart."""
+    c = Case(19, [260], [260], 4, 2, 128)
+    want, lse, _ = c.run(True)
+    for name, h in (("q", 4), ("k", 2), ("v", 2)):
+        x = getattr(c, name)
+        far = torch.empty(260 * 8_400_000, dtype=torch.bfloat16, device=DEV).as_strided((260, h, 128), (8_400_000, 128, 1))
+        setattr(c, name, far.copy_(x))
+        o, l2, _ = c.run(True)
+        assert torch.equal(o, want) and torch.equal(l2, lse)
+        setattr(c, name, x)
+
+
 def test_long_prompt_sampled():
     """One 5000-token prompt: the heads of the first group against the oracle."""
     c = Case(17, [5000], [5000], 32, 8, 128)

@@ -398,3 +398,27 @@ def test_append_on_another_stream_and_strided_inputs():
     c.run(rope_dim=128, stream=stream)
     c.k_cache, c.v_cache = c.k_cache.contiguous(), c.v_cache.contiguous()
     _check_append(c, before, before_scales, 128, "interleaved")
+
+
+def test_rows_past_32_bit_offsets():
+    """Tokens 8.4 million values apart, read, turned in place and appended (bf16 pages as far apart)."""
+    rng = np.random.default_rng(16)
+    n, hk, d, page = 260, 2, 128, 16
+    far = torch.zeros(n * 8_400_000, dtype=torch.bfloat16, device=DEV)
+    x = torch.from_numpy(rng.standard_normal((n, hk, d)).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    spread = far.as_strided((n, hk, d), (8_400_000, d, 1))
+    spread.copy_(x)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    want, _ = skv.rope_apply(x, None, pos)
+    got, _ = skv.rope_apply(spread, None, pos)
+    assert torch.equal(got, want)
+    pages = -(-n // page)
+    table = [torch.tensor(a, dtype=torch.int32, device=DEV) for a in ([0, n], [0, pages], list(range(pages))[::-1], [n - (pages - 1) * page])]
+    dense = [torch.zeros(pages, page, hk, d, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    skv.paged_kv_append(x, x, *dense, *table, rope_dim=d)
+    cache = [far[at:].as_strided((pages, page, hk, d), (130_000_000, 512, 128, 1)) for at in (1024, 1024 + 256)]
+    skv.paged_kv_append(spread, x, *cache, *table, rope_dim=d)
+    for a, b in zip(dense, cache):
+        assert torch.equal(a, b)
+    skv.rope_apply(spread, None, pos, q_out=spread)
+    assert torch.equal(spread, want)

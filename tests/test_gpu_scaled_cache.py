@@ -183,6 +183,41 @@ def test_zero_scales_everywhere():
     assert np.allclose(lse.cpu().numpy(), np.log([[40.0], [3.0]]), atol=1e-5)
 
 
+@pytest.mark.parametrize("cache,page,block", [("e4m3", 16, 16), ("i8", 16, 16), ("e4m3", 12, 4), ("i8", 12, 4)])
+def test_subnormal_scales_count_as_zero(cache, page, block):
+    c = Case(7, [40, 100, 3], [1, 2, 1], 8, 2, 64, page, block, cache, poison=False)
+    k, v, ks, vs = c.device()
+    outs = []
+    for tiny in (1e-39, 0.0):
+        ks[::3], vs[::2] = tiny, tiny                      # whole pages, beside others of ordinary scales
+        outs.append(_run(c, False, (k, v, ks, vs))[:2])
+    assert bool(torch.isfinite(outs[0][0]).all()) and bool(torch.isfinite(outs[0][1]).all())
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("cache,block", [("i8", 16), ("e4m3", 4)])
+def test_append_and_attention_past_32_bit_offsets(cache, block):
+    """Pages 1.2e9 bytes apart: the same results as in a dense cache."""
+    rng = np.random.default_rng(15)
+    hq, hk, d, page, pages, n = 8, 2, 64, 16, 3, 45
+    far = torch.zeros(2 * 1_200_000_000 + (1 << 16), dtype=torch.uint8, device=DEV)
+    spread = lambda at: far[at:].as_strided((pages, page, hk, d), (1_200_000_000, 256, 64, 1)).view(CODE[cache])  # noqa: E731
+    results = []
+    k, v, q = (torch.from_numpy(rng.standard_normal((n, h, d)).astype(np.float32)).to(torch.bfloat16).to(DEV) for h in (hk, hk, hq))
+    ids = _i32([2, 0, 1])
+    for dense in (True, False):
+        kc, vc = ((torch.zeros(pages, page, hk, d, dtype=CODE[cache], device=DEV) for _ in range(2)) if dense else
+                  (spread(0), spread(128)))
+        ks, vs = (torch.zeros(pages, page // block, hk, device=DEV) for _ in range(2))
+        skv.paged_kv_append(k, v, kc, vc, _i32([0, n]), _i32([0, 3]), ids, _i32([n - 32]), k_scale=ks, v_scale=vs,
+                            rope_dim=d)
+        o, lse, _ = skv.paged_attention_scaled(q, kc, vc, ks, vs, [0, n], [0, 3], ids, [n - 32], causal=True)
+        results.append((o, lse, ks, vs, kc.view(torch.uint8).contiguous(), vc.view(torch.uint8).contiguous()))
+    assert int(results[0][4].ne(0).sum()) > 0.9 * n * hk * d
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
 def test_strided_caches_scales_and_outputs_given():
     c = Case(7, [100, 33, 0, 250], [1, 2, 1, 1], 16, 4, 128, 16, 8, "e4m3")
     k, v, ks, vs = c.device()

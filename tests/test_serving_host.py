@@ -79,6 +79,20 @@ def test_append_refusals(change, code):
     assert skv._kv_append(ctypes.byref(_append_params(**change)), None) == code
 
 
+@pytest.mark.parametrize("change", [dict(q_out_stride=(0, 64)), dict(q_out_stride=(512, 0)), dict(k_out_stride=(128, 0))])
+def test_rotated_rows_need_places_of_their_own(change):
+    assert skv._rope_apply(ctypes.byref(_rope_params(**change)), None) == skv.ERR_INVALID
+
+
+@pytest.mark.parametrize("change", [
+    dict(q_out_stride=(0, 64)), dict(k_stride=(0, 128, 64)), dict(v_stride=(2048, 0, 64)), dict(k_stride=(2048, 128, 0)),
+    dict(kv_dtype=skv.I8, block_tokens=8, k_scale_stride=(0, 2, 1)),
+    dict(kv_dtype=skv.I8, block_tokens=8, v_scale_stride=(4, 0, 1)),
+    dict(kv_dtype=skv.E4M3, block_tokens=8, v_scale_stride=(4, 2, 0))])
+def test_appended_rows_and_scales_need_places_of_their_own(change):
+    assert skv._kv_append(ctypes.byref(_append_params(**change)), None) == skv.ERR_INVALID
+
+
 def test_null_params():
     assert skv._rope_apply(None, None) == skv.ERR_INVALID
     assert skv._kv_append(None, None) == skv.ERR_INVALID
@@ -380,6 +394,25 @@ def test_prompt_fwd_needs_its_own_plan():
     assert skv._scaled_fwd(ctypes.byref(_scaled_params()), PTR, ctypes.byref(info), None) == skv.ERR_INVALID
     with pytest.raises(ValueError):
         skv.plan_prompt([0, 5], [0, 5, 6], 4, 2, 64)
+
+
+def test_a_kept_plan_serves_the_requests_it_was_made_for():
+    torch = pytest.importorskip("torch")
+    q, k = torch.zeros(9, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 2, 64, dtype=torch.bfloat16)
+    for plan, qo, kv, causal in ((skv.plan_prompt([0, 8], None, 4, 2, 64), [0, 9], None, True),
+                                 (skv.plan_prompt([0, 9], None, 8, 2, 64), [0, 9], None, True),
+                                 (skv.plan_prompt([0, 9], [0, 8], 4, 2, 64), [0, 9], None, True),
+                                 (skv.plan_prompt([0, 9], None, 4, 2, 64), [0, 9], None, False),
+                                 (skv.plan_prompt([0, 9], None, 4, 2, 64), [0, 4, 9], None, True)):
+        with pytest.raises(ValueError, match="plan was made for"):
+            skv.prompt_attention(q, k, k, qo, kv, causal=causal, plan=plan)
+    cache, scale = torch.zeros(3, 16, 2, 64, dtype=torch.int8), torch.zeros(3, 1, 2)
+    for plan, qo, causal in ((skv.plan_paged_scaled([0, 1], [0, 2], [5], 16, 4, 2, 64), [0, 2], False),
+                             (skv.plan_paged_scaled([0, 1], [0, 2], [5], 16, 8, 2, 64), [0, 1], False),
+                             (skv.plan_paged_scaled([0, 1], [0, 2], [5], 8, 4, 2, 64), [0, 1], False),
+                             (skv.plan_paged_scaled([0, 1], [0, 2], [5], 16, 4, 2, 64), [0, 1], True)):
+        with pytest.raises(ValueError, match="plan was made for"):
+            skv.paged_attention_scaled(q, cache, cache, scale, scale, qo, [0, 2], None, [5], causal=causal, plan=plan)
 
 
 def test_prompt_struct_layout():

@@ -10,15 +10,18 @@
 // its threads, one 16-value item of a row each.
 //
 // Block-scaled caches (append_blocks_kernel): the unit is a segment -- the new tokens of one
-// request that fall into one scale block -- of K or of V.  A block of sixteen warps forms the segment's
+// request that fall into one scale block -- of K or of V.  A block of eight warps forms the segment's
 // (cos, sin) table once and goes through the heads, as many at a time as the segment's length leaves
-// warps for (one warp a head for a few tokens, all sixteen for 64): take the maximum of the head's
-// (rotated) rows, settle the scale, re-encode the block's other codes if the scale grew, encode the
-// rows from registers while the next heads' rows are on their way.  Segments of more than 64 tokens
-// are read twice.  One owner per (block, head): no atomics, results do not depend on order.  Window w
+// warps for (one warp a head up to 16 tokens of 128 values, four for 64; a lane holds up to four items
+// of 16 values): take the maximum of the head's (rotated) rows, settle the scale, encode the rows from
+// registers while the next heads' rows are on their way, re-encode the block's other codes if the scale
+// grew.  Segments of more than 64 tokens are read twice.  One owner per (block, head): no atomics, results do not depend on order.  Window w
 // of the grid takes the segments that begin among its rows; the last blocks of the grid rotate Q.
 // (One warp per head, two passes over its rows: 93 us for 18 k tokens, 8 heads of 128, blocks of 64;
-// eight warps for two heads, each with its own search and table: 121 us; this form: 43 us.)
+// eight warps for two heads, each with its own search and table: 121 us; sixteen warps a segment, one
+// item a lane: 43 us, and 5.9 us for a step of 64 tokens; this form: 39 and 5.1 us.  A segment takes 13
+// (V) to 20 us (K), two to an SM at a time: 1.4 us until its place is known, 4 for the table, then 3 us
+// for every two heads.)
 #include "rope.cuh"
 
 #include <cuda_fp8.h>
@@ -32,7 +35,8 @@ namespace {
 using rope::Freq;
 
 constexpr int kRowThreads = 256;
-constexpr int kBlockWarps = 16;  // block kernel
+constexpr int kBlockWarps = 8;   // block kernel
+constexpr int kLaneRows = 4;     // rows of a chunk that a lane holds, block kernel
 constexpr int kMaxPairs = 64;    // head_dim <= 128
 constexpr int kMaxTokens = 16;   // tokens per block of threads, row kernel
 constexpr int kTableTokens = 64; // tokens whose tables are held at once, block kernel
@@ -61,7 +65,7 @@ struct AppendArgs {
   int batch, num_rows, num_pages, page_size, hk, hq, head_dim, block_tokens;
   int per_block;        // rows of a window
   int per_q_block;      // rows of a block of threads that rotates Q beside the block kernel
-  int num_windows, stripe, num_kv_blocks;
+  int num_windows;
   float inv_scale;
   Freq f;
 };
@@ -113,13 +117,15 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
-__device__ __forceinline__ uint32_t i8_code(float x) {  // rn, [-127, 127], NaN -> 0
-  const int c = __float2int_rn(fminf(fmaxf(x, -127.f), 127.f));
-  return (uint32_t)(x == x ? c : 0) & 0xFFu;
+// An int8 code (rn, [-127, 127], NaN -> 0) in the low byte: 1.5 x 2^23 leaves a float's last bits integral.
+// (The conversion instruction runs at a quarter of the rate: 47 us against 44 at the size above.)
+__device__ __forceinline__ uint32_t i8_code(float x) {
+  return __float_as_uint(fminf(fmaxf(x == x ? x : 0.f, -127.f), 127.f) + 12582912.f);
 }
 template <bool I8>
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  if constexpr (I8) return i8_code(a) | (i8_code(b) << 8) | (i8_code(c) << 16) | (i8_code(d) << 24);
+  if constexpr (I8)
+    return __byte_perm(__byte_perm(i8_code(a), i8_code(b), 0x0040), __byte_perm(i8_code(c), i8_code(d), 0x0040), 0x5410);
   else return e4m3x4(a, b, c, d);
 }
 // An item's 16 codes: 8 bytes for each chunk.
@@ -260,8 +266,9 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int items = a.head_dim / 16, item = lane % items, lt = 32 / items;
   int g = 1;  // warps of a head
-  while (g < kBlockWarps && min(cnt, kTableTokens) > g * lt) g *= 2;
-  const int part = warp & (g - 1), sub = part * lt + lane / items;  // this lane's row of a chunk
+  while (g < kBlockWarps && min(cnt, kTableTokens) > g * lt * kLaneRows) g *= 2;
+  const int part = warp & (g - 1), sub = part * lt + lane / items;  // this lane's first row of a chunk
+  const int step = g * lt;  // rows between a lane's
   const int nrot = a.f.dim / 16, stride4 = rope::table_float4s(a.f.dim);
   const rope::Item it = rope::item_of(item, TURN == kCopy ? 0 : a.f.dim, a.head_dim);
   const int64_t src_row = V ? a.v0 : a.k0, dst_row = V ? a.vc1 : a.kc1;
@@ -269,9 +276,14 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
   const int heads = kBlockWarps / g, h0 = warp / g;
   const __nv_bfloat16* src = row_ptr<V>(a, t0 + sub, h0);
   const int64_t src_head = heads * (V ? a.v1 : a.k1);
-  rope::Raw<__nv_bfloat16> raw;
-  float x[16];
-  auto mine = [&](int c0) { return sub < (ONCE ? cnt : min(cnt - c0, kTableTokens)); };
+  rope::Raw<__nv_bfloat16> raw[kLaneRows];
+  float x[kLaneRows][16];
+  auto mine = [&](int c0, int i) { return sub + i * step < (ONCE ? cnt : min(cnt - c0, kTableTokens)); };
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i)
+      if (mine(c0, i)) raw[i].load(src + (c0 + i * step) * src_row, it);
+  };
   auto fill = [&](int c0) {
     if (TURN == kCopy) return;
     const int n = min(cnt - c0, kTableTokens);
@@ -282,11 +294,19 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     rope::fill_table(table, sh.pos, n, sh.turns, a.f.dim, a.f.mscale, TURN == kHalves, tid, threads);
     __syncthreads();
   };
-  auto turn = [&]() {  // raw -> x, for a lane with a row
-    raw.values(x);
-    if (TURN != kCopy && it.turned) rope::turn_item(x, table + sub * stride4, item, nrot, TURN == kHalves);
+  auto turn = [&](int c0, float top) {  // raw -> x, and the largest of them
+#pragma unroll
+    for (int i = 0; i < kLaneRows; ++i) {
+      if (!mine(c0, i)) continue;
+      raw[i].values(x[i]);
+      if (TURN != kCopy && it.turned)
+        rope::turn_item(x[i], table + (sub + i * step) * stride4, item, nrot, TURN == kHalves);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[i][e]));
+    }
+    return top;
   };
-  if (ONCE && h0 < a.hk && mine(0)) raw.load(src, it);
+  if (ONCE && h0 < a.hk) load(0);
   if (!sound_page(a, page, lane)) return;  // the same for every warp
   if (ONCE) fill(0);
   float* scale = scale_ptr<V>(a, page, blk, h0);
@@ -294,16 +314,15 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
   uint8_t* dst = cache_ptr<V>(a, page, first, h0);
   const int64_t dst_head = heads * (V ? a.vc2 : a.kc2);
   auto store = [&](int c0, float inv) {
-    uint2 code[2];
-    encode_item<I8>(x, inv, code);
-    uint8_t* row = dst + (old + c0 + sub) * dst_row;
-    *reinterpret_cast<uint2*>(row + it.c0) = code[0];
-    *reinterpret_cast<uint2*>(row + it.c1) = code[1];
-  };
-  auto largest = [&](float top) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
-    return top;
+    for (int i = 0; i < kLaneRows; ++i) {
+      if (!mine(c0, i)) continue;
+      uint2 code[2];
+      encode_item<I8>(x[i], inv, code);
+      uint8_t* row = dst + (old + c0 + sub + i * step) * dst_row;
+      *reinterpret_cast<uint2*>(row + it.c0) = code[0];
+      *reinterpret_cast<uint2*>(row + it.c1) = code[1];
+    }
   };
   int odd = 0;
 #pragma unroll 1
@@ -312,19 +331,18 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     const float before = live && old > 0 ? *scale : 0.f;
     float top = 0.f;
     if constexpr (ONCE) {
-      if (live && mine(0)) {
-        turn();
-        top = largest(0.f);
-        if (h + heads < a.hk) raw.load(src += src_head, it);  // the next heads' rows
+      if (live) {
+        top = turn(0, 0.f);
+        src += src_head;
+        if (h + heads < a.hk) load(0);  // the next heads' rows
       }
     } else {
 #pragma unroll 1
       for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
         fill(c0);
-        if (!live || !mine(c0)) continue;
-        raw.load(src + c0 * src_row, it);
-        turn();
-        top = largest(top);
+        if (!live) continue;
+        load(c0);
+        top = turn(c0, top);
       }
     }
     uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // of values >= 0: order as integers
@@ -339,14 +357,14 @@ __device__ __forceinline__ void segment(const AppendArgs& a, int t0, int cnt, in
     __syncwarp();
     if (live && lane == 0 && part == 0) *scale = after;
     if constexpr (ONCE) {
-      if (live && mine(0)) store(0, inv);
+      if (live) store(0, inv);
     } else {
 #pragma unroll 1
       for (int c0 = 0; c0 < cnt; c0 += kTableTokens) {
         fill(c0);
-        if (!live || !mine(c0)) continue;
-        raw.load(src + c0 * src_row, it);
-        turn();
+        if (!live) continue;
+        load(c0);
+        turn(c0, 0.f);
         store(c0, inv);
       }
       src += src_head;
@@ -404,14 +422,14 @@ template <bool I8, int TURN, bool LONG>
 __global__ void __launch_bounds__(32 * kBlockWarps, 2) append_blocks_kernel(const __grid_constant__ AppendArgs a) {
   extern __shared__ float4 table[];
   __shared__ BlockShared sh;
-  // stripes of one block per SM, K's and V's in turns: an SM gets as many of the one as of the other
-  const int b = blockIdx.x, stripe = b / a.stripe, window = (stripe >> 1) * a.stripe + b % a.stripe;
-  if (b < a.num_kv_blocks) {
-    if (window >= a.num_windows) return;
-    if (stripe & 1) window_segments<I8, true, kCopy, LONG>(a, window, table, sh);
-    else window_segments<I8, false, TURN, LONG>(a, window, table, sh);
+  // K's windows first: they take longer (a table, rotation), so V's even out the launch's end
+  const int b = blockIdx.x;
+  if (b < a.num_windows) {
+    window_segments<I8, false, TURN, LONG>(a, b, table, sh);
+  } else if (b < 2 * a.num_windows) {
+    window_segments<I8, true, kCopy, LONG>(a, b - a.num_windows, table, sh);
   } else {
-    const int t0 = (b - a.num_kv_blocks) * a.per_q_block;
+    const int t0 = (b - 2 * a.num_windows) * a.per_q_block;
     rows_pass<MODE_NONE, 32 * kBlockWarps>(a, t0, min(a.per_q_block, a.num_rows - t0), table);
   }
 }
@@ -492,14 +510,12 @@ int launch_kv_append(const skv_append_params& p, cudaStream_t s) {
     return (int)cudaGetLastError();
   }
   // windows of one row while there are few, then three an SM for each of K and V: two blocks are
-  // resident, and the third evens out what segments of unlike lengths leave (one, two, three, four an
-  // SM: 50.8, 49.0, 43.2, 45.2 us at the size that the top names)
+  // resident, and the third evens out what segments of unlike lengths leave (two, three, four, five an
+  // SM: 45.6, 40.6, 42.8, 44.9 us at the size that the top names; K's and V's windows in turns: 42.8)
   a.per_block = (int)std::max<int64_t>(1, p.num_rows / (sms * 3));
   a.num_windows = cdiv(p.num_rows, a.per_block);
   a.per_q_block = 1;
-  a.stripe = (int)std::min<int64_t>(sms, a.num_windows);
-  a.num_kv_blocks = 2 * a.stripe * cdiv(a.num_windows, a.stripe);
-  int blocks = a.num_kv_blocks;
+  int blocks = 2 * a.num_windows;
   if (a.hq > 0) {
     a.per_q_block = rope::tokens_per_block(p.num_rows, a.hq * items, 32 * kBlockWarps, kMaxTokens, sms);
     blocks += cdiv(p.num_rows, a.per_q_block);

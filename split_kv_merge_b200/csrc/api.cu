@@ -47,6 +47,8 @@ struct PersistOpts {
   int32_t tile_tokens = 128;
   int32_t page_size = 1;
   int32_t piece_cost = 0;  // fixed cost of a work item (query load, pipeline refill, epilogue), in tiles
+  int32_t min_piece = 4;   // tiles of the smallest piece of slices of 16 tiles or more (of shorter ones: 4); a
+                           // shorter rest joins the slice before
   // CTAs per KV slice.  With group > 1 the work items cover query tile 0 only and every slice is
   // run by `group` co-resident CTAs, each taking one (query tile, head group) of every item, so
   // the slice streams from HBM about once and the other CTAs read it from L2.  The plan's
@@ -119,7 +121,7 @@ skv_status plan_common(int32_t batch, const std::vector<ReqShape>& req, const st
     // piece per request plus one per CTA boundary (charged at the mean)
     if (nonempty > 0) total += piece_total + (double)(G - 1) * piece_total / (double)nonempty;
     const double target = total / G;
-    const int64_t min_piece = std::max<int64_t>(1, std::min<int64_t>(4, (int64_t)target));
+    const int64_t min_piece = std::max<int64_t>(1, std::min<int64_t>(target < 16 ? 4 : po.min_piece, (int64_t)target));
     int cta = 0;
     double cum = 0;
     for (int32_t r = 0; r < batch; ++r) {
@@ -591,7 +593,10 @@ skv_status skv_plan_paged_scaled(int32_t batch, const int32_t* qo_indptr_h, cons
   po.page_size = page_size;
   po.tile_tokens = gqa_scaled_tile_tokens(num_kv_heads);
   po.flat_ctas = std::max(1, device_sms(policy == SKV_SPLIT_BALANCED ? param : 0) / units);
+  // no slice takes more than its share (64-request e4m3 decode 104.5 -> 101.7 us, verification of four
+  // tokens over 16 long requests 77.4 -> 75.5, against pieces of four tiles at least)
   po.piece_cost = 2;
+  po.min_piece = 1;
   st = plan_common(batch, req, kv_len, gqa_scaled_q_tile(group, max_q), 1, 8, policy, param, split_indptr_h,
                    split_bounds_h, KERNEL_GQA_SCALED, po, plan_h, plan_capacity, info);
   if (st != SKV_OK) return st;

@@ -15,7 +15,9 @@
 //     groups of 8 tokens (one scale per group and head is staged);
 //   - else by cp.async from four warps (any page size, block size and 16-byte strides; one scale per
 //     token and head).  Measured on the 64-request 64/8-head e4m3 decode, pages of 16: 225 us
-//     against 106 us by TMA: address arithmetic for 4096 copies a stage holds the ring back.
+//     against 102 us by TMA (6.3 TB/s): address arithmetic for 4096 copies a stage holds the ring back.
+// With several query tokens the consumers bind it: 4 tokens over 171 k int8 tokens in pages of 64, 32/8
+// heads: 76 us (4.6 TB/s), issue slots 46 % busy, most of it widening and the softmax of 16 rows.
 //
 // Decode has few query rows per KV head (R = group x query tokens <= 16), far below the 128 rows of
 // the tcgen05 shapes, and each code needs widening in registers anyway, so the products are

@@ -28,10 +28,11 @@
 // Persistent: the planner hands every CTA a list of items (a pair of query tiles and a range of
 // key tiles), longest first onto the least loaded.  Items of few rows over many keys, and a few of
 // those that would make no full round, are cut along the keys into fp32 partials that the merge pass
-// joins.  An item's end costs about 6000 cycles (the last P V, its results, the next item's first
-// scores): its code runs once in a while and is kept short, and results leave as whole lines (16
-// sequences of 64 .. 2048 tokens: 218 -> 203 us).  Roles: warps 0-3 softmax of A, 4-7 of B,
-// warp 8 TMA (ring of K and V tiles in the order of use), warps 9 and 10 the MMAs of A and of B.
+// joins.  An item's end costs about 5000 cycles (the last P V, its results, the next item's first
+// scores): its code runs once in a while and is kept short, and results leave by whole sectors (16
+// sequences of 64 .. 2048 tokens: 194 us, 204 with 16-byte stores, 218 with all of it unrolled).
+// Roles: warps 0-3 softmax of A, 4-7 of B, warp 8 TMA (ring of K and V tiles in the order of use),
+// warps 9 and 10 the MMAs of A and of B.
 // All waits are bounded.
 #include <cudaTypedefs.h>
 
@@ -140,23 +141,15 @@ __device__ __forceinline__ void weights(const float (&s)[kTile], uint64_t sc2, u
   }
 }
 
-// 32 words of a row in every lane become whole lines: an 8 x 8 transposition of 16-byte chunks
-// among 8 lanes, after which lane i of them holds chunk i of their rows 0..7 (chunk c of `u`: row c).
-__device__ __forceinline__ void transpose8(uint32_t (&u)[32], int lane) {
-#pragma unroll
-  for (int b = 1; b < 8; b <<= 1) {
-    const bool hi = lane & b;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c & b) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t &lo_w = u[c * 4 + e], &hi_w = u[(c + b) * 4 + e];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? lo_w : hi_w, b);
-        if (hi) lo_w = got;
-        else hi_w = got;
-      }
-    }
+// 32 bytes, one whole sector, in one store where the address allows it (`whole`)
+__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8], bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 }
 
@@ -479,57 +472,36 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       float* const lse = part ? a.lse_part : a.lse;
       if (r < rows && lse != nullptr)
         lse[(row0 + r * step) * a.hq + s_me.head] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
-      // 128 bytes of a row at a time, turned so that eight lanes write them
-      auto store = [&](uint32_t (&u)[32], void* base, int64_t row_bytes, int byte) {
-        transpose8(u, lane);
-        uint8_t* dst = static_cast<uint8_t*>(base) + byte + (lane & 7) * 16;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int row = quarter * 32 + (lane & 24) + c;
-          if (row < rows)
-            *reinterpret_cast<uint4*>(dst + row * row_bytes) = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
-        }
-      };
-      auto load_o = [&](int c, float (&v)[16]) {  // the whole warp loads
-        if (tiles > 0) {
+      const bool fp32 = part || sizeof(OutT) == 4;
+      const int64_t out = ((row0 + r * step) * a.hq + s_me.head) * D;
+      uint8_t* dst = part ? reinterpret_cast<uint8_t*>(a.o_part + out)
+                          : reinterpret_cast<uint8_t*>(reinterpret_cast<OutT*>(a.o) + out);
+      const bool whole = (reinterpret_cast<uintptr_t>(part ? a.o_part : a.o) & 31) == 0;  // rows are whole sectors
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        float v[16];
+        if (tiles > 0) {  // the whole warp loads; live rows store
           tc::tmem_ld_x16(to + c, v);
           tc::tmem_wait_ld();
         }
+        uint32_t u[8], u2[8];
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = some ? v[e] * inv : 0.f;
-      };
-      const int64_t out0 = (row0 * a.hq + s_me.head) * D;
-      if (part || sizeof(OutT) == 4) {
-        float* base = (part ? a.o_part : reinterpret_cast<float*>(a.o)) + out0;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t u[32];
+        if (fp32) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 16) {
-            float v[16];
-            load_o(c + k, v);
+          for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(v[e]), u2[e] = __float_as_uint(v[8 + e]);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) u[k + e] = __float_as_uint(v[e]);
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+            u[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
-          store(u, base, step * a.hq * D * 4, c * 4);
         }
-      } else {
-        OutT* base = reinterpret_cast<OutT*>(a.o) + out0;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 64) {
-          uint32_t u[32];
-#pragma unroll
-          for (int k = 0; k < 64; k += 16) {
-            float v[16];
-            load_o(c + k, v);
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(v[e], v[e + 1]);
-              u[(k + e) >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-          }
-          store(u, base, (int64_t)a.hq * D * 2, c * 2);
+        if (r < rows) {
+          store32(dst, u, whole);
+          if (fp32) store32(dst + 32, u2, whole);
         }
+        dst += fp32 ? 64 : 32;
       }
       tc::tc_fence_before();  // O has been read before the next item's first P is announced
     }

@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int rows_per_pass = kThreads / a.items;
   const int item = tid % a.items;
   const rope::Item it = rope::item_of(item, a.f.dim, a.head_dim);
-  const int heads = a.hq + a.hk, rows = n * heads;
-  int row = tid / a.items;
+  const int heads = a.hq + a.hk;
+  const int row = tid / a.items;
   const bool active = row < rows_per_pass;
 
   // the first rows' loads go out before the table is formed
@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <typename T>
 int launch(const RopeArgs& a, cudaStream_t s) {
   const int smem = a.per_block * a.f.dim * 4;  // <= 16 KB: below the default limit
-  rope_kernel<T><<<(a.tokens + a.per_block - 1) / a.per_block, kThreads, smem, s>>>(a);
+  const int blocks = (int)(((int64_t)a.tokens + a.per_block - 1) / a.per_block);
+  rope_kernel<T><<<blocks, kThreads, smem, s>>>(a);
   return (int)cudaGetLastError();
 }
 

@@ -124,6 +124,18 @@ def test_rows_behind_the_last_sequence_are_left():
     assert bool(torch.all(o[123:] == 5.0)) and bool(torch.all(lse[123:] == 5.0))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_outputs_on_16_byte_addresses(dtype):
+    """Results at an address that is a multiple of 16 bytes but not of 32."""
+    c = Case(21, [33, 200], [33, 200], 4, 2, 64)
+    want, lse, _ = c.run(True, o_dtype=dtype)
+    flat = torch.zeros(233 * 4 * 64 + 32, dtype=dtype, device=DEV)
+    out = flat[16 // flat.element_size():][:233 * 4 * 64].view(233, 4, 64)
+    assert out.data_ptr() % 32 == 16
+    c.run(True, o_out=out)
+    assert torch.equal(out, want) and int(flat.ne(0).sum()) == int(want.ne(0).sum())
+
+
 def test_slices_of_one_projection():
     rng = np.random.default_rng(9)
     qkv = torch.from_numpy(rng.standard_normal((321, 16, 128)).astype(np.float32)).to(torch.bfloat16).to(DEV)

@@ -275,3 +275,53 @@ def test_a_serving_step():
         rel = np.linalg.norm(o.cpu().numpy() - O) / np.linalg.norm(O)
         # bf16 rotated rows and weights (2^-8 each) in the prompt; half a 127th of about 4 sigma in the int8 cache
         assert rel < (2.0 ** -6 if step == 0 else 4 / 127), (step, rel)
+
+
+def test_two_captured_steps_side_by_side():
+    """Two graphs of a whole step (append, rotation, both attentions) replayed on two streams at once."""
+    lens, page, hq, hk, d = np.array([37, 130]), 16, 8, 2, 128
+    n, pages = int(lens.sum()), -(-lens // page)
+    qo, ki, la = np.concatenate([[0], np.cumsum(lens)]), np.concatenate([[0], np.cumsum(pages)]), lens - (pages - 1) * page
+    i32 = lambda a: torch.tensor(np.asarray(a, dtype=np.int32), device=DEV)  # noqa: E731
+    qo_d, ki_d, ids, la_d = i32(qo), i32(ki), i32(np.arange(ki[-1])), i32(la)
+    pos = i32(np.concatenate([np.arange(x) for x in lens]))
+    scaled = skv.plan_paged_scaled(qo, ki, la, page, hq, hk, d, True).to(DEV)
+    packed = skv.plan_prompt(qo, None, hq, hk, d, True).to(DEV)
+
+    def make(seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        x = [torch.randn(n, h, d, device=DEV, generator=g).bfloat16() for h in (hq, hk, hk)]
+        x += [torch.zeros(int(ki[-1]), page, hk, d, dtype=torch.int8, device=DEV) for _ in range(2)]
+        return x + [torch.zeros(int(ki[-1]), 2, hk, device=DEV) for _ in range(2)]
+
+    def step(q, k, v, kc, vc, ks, vs):
+        qr = skv.paged_kv_append(k, v, kc, vc, qo_d, ki_d, ids, la_d, k_scale=ks, v_scale=vs, q=q, rope_dim=d)
+        _, kr = skv.rope_apply(None, k, pos)
+        a = skv.paged_attention_scaled(qr, kc, vc, ks, vs, qo, ki, ids, la, causal=True, plan=scaled, kv_indptr=ki_d,
+                                       kv_last_page_len=la_d)
+        b = skv.prompt_attention(qr, kr, v, qo, plan=packed)
+        return a[0], a[1], b[0], b[1]
+
+    sets = [make(1), make(2)]
+    want = [[t.clone() for t in step(*s)] for s in sets]
+    torch.cuda.synchronize()
+    streams, graphs, outs = [torch.cuda.Stream() for _ in sets], [], []
+    for s, stream in zip(sets, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            outs.append(step(*s))
+    for _ in range(10):
+        for s in sets:
+            for t in s[3:]:
+                t.zero_()
+        for o in outs:
+            for t in o:
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            for x, y in zip(o, w):
+                assert torch.equal(x, y)

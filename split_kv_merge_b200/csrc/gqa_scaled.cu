@@ -31,9 +31,13 @@
 //   - chunks are XOR-swizzled by token so that the eight lanes of a 128-byte wavefront hit
 //     different banks, for K and V alike.
 // Precision: Q (bf16) moves to f16 after a power-of-two scale per row (largest element to
-// [2^14, 2^15): exact for every element of at least 2^-31 of the row's largest).  Weights are formed as
-// p * (vs / vref), vref the largest vs of the 32 tokens, in f16 (11 bits; the maximum is raised
-// once a score passes it by 2^8, so p <= 2^8), and the partial product is scaled by vref in fp32.
+// [2^14, 2^15): exact for every element of at least 2^-31 of the row's largest).  Weights w = p vs are
+// formed in fp32 and go to f16 relative to the largest w that the row has among the warp's 32 tokens,
+// masked ones left out (w / wmax x 2^14: 11 bits down to 2^-28 of wmax, then a 2^-39th of it), and the
+// partial product is scaled by wmax in fp32.  So neither a block that a row does not see nor one that
+// it hardly attends to costs another block bits, and a key that outweighs all others has the weight
+// 2^14 exactly.  The divisor is the fp32 sum of the exact p: the rounded w do not tell p apart where
+// vs is 0 or far below its neighbours'.  (The maximum is raised once a score passes it by 2^8: p <= 2^8.)
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -56,6 +60,8 @@ constexpr int kConsumerRegs = 208, kProducerRegs = 88;
 static_assert(256 * kConsumerRegs + 128 * kProducerRegs <= kThreads * 168, "the split fits the launch's registers");
 constexpr int kWarpTokens = 32;               // tokens of a stage that one consumer warp takes
 constexpr float kRaise = 8.f;
+constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126
+constexpr float kWeightTop = 16384.f;         // a row's largest weight of 32 tokens in f16
 
 template <int D>
 struct Smem {
@@ -519,7 +525,7 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         // a masked -inf stays one; at 1e-30 every score of the block is 0 in any case)
         const int ta = col_token<D>(2 * t), tc1 = col_token<D>(2 * t + 1);
         float vsc[4][kTokScales], f[kRowSets][4][kTokScales];
-        float mx[2] = {-INFINITY, -INFINITY}, vref = 0.f;
+        float mx[2] = {-INFINITY, -INFINITY};
         if (tb + kWarpTokens > all_see) {
 #pragma unroll
           for (int n = 0; n < 4; ++n)
@@ -535,8 +541,8 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           for (int e = 0; e < kTokScales; ++e) {  // TMA: one scale for the 8 tokens
             const int at = TMA ? 4 * n : (8 * n + (e ? tc1 : ta)) * 4;
             const float ks = lds_f(kss + at);
-            vsc[n][e] = lds_f(vss + at);
-            vref = fmaxf(vref, vsc[n][e]);
+            const float vs = lds_f(vss + at);
+            vsc[n][e] = vs < kTinyScale ? 0.f : vs;  // subnormal scales count as 0
 #pragma unroll
             for (int r = 0; r < kRowSets; ++r) f[r][n][e] = fmaxf(ks * sc[r], 1e-30f);
           }
@@ -548,8 +554,6 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
               mx[r] = fmaxf(mx[r], fmaxf(s[n][2 * r] * f[r][n][0], s[n][2 * r + 1] * f[r][n][kTokScales - 1]));
           }
         }
-        if constexpr (!TMA) vref = quad_max(vref);
-        const float rv = vref >= 1.17549435e-38f ? 1.f / vref : 0.f;  // subnormal scales count as 0
         bool raise = false;
 #pragma unroll
         for (int r = 0; r < kRowSets; ++r) {
@@ -570,24 +574,31 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
           }
         }
-        // ---- weights
+        // ---- weights w = p vs and the row's largest; in f16 relative to it
+        float wmax[2] = {0.f, 0.f}, wmul[kRowSets], vmul[kRowSets];
+#pragma unroll
+        for (int r = 0; r < kRowSets; ++r) {
+          const float nm = m[r] == -INFINITY ? 0.f : -m[r];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float p0 = ex2f(fmaf(s[n][2 * r], f[r][n][0], nm));
+            const float p1 = ex2f(fmaf(s[n][2 * r + 1], f[r][n][kTokScales - 1], nm));
+            l[r] += p0 + p1;
+            s[n][2 * r] = p0 * vsc[n][0];
+            s[n][2 * r + 1] = p1 * vsc[n][kTokScales - 1];
+            wmax[r] = fmaxf(wmax[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
+          }
+          wmax[r] = quad_max(wmax[r]);
+          wmul[r] = fminf(__fdividef(kWeightTop, wmax[r]), 1.f / kTinyScale);  // finite for wmax = 0
+          vmul[r] = fmaxf(wmax[r] * (1.f / kWeightTop), kTinyScale) * (I8 ? 1.f / kI8Unit : 1.f);
+        }
         uint32_t pf[2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float v0 = vsc[n][0] * rv, v1 = kTokScales == 1 ? v0 : vsc[n][kTokScales - 1] * rv;
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (r < kRowSets) {
-              const float nm = m[r] == -INFINITY ? 0.f : -m[r];
-              const float p0 = ex2f(fmaf(s[n][2 * r], f[r % kRowSets][n][0], nm));
-              const float p1 = ex2f(fmaf(s[n][2 * r + 1], f[r % kRowSets][n][kTokScales - 1], nm));
-              l[r] += p0 + p1;
-              pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * v0, p1 * v1);
-            } else {
-              pf[n >> 1][(n & 1) * 2 + r] = 0u;
-            }
-          }
-        }
+          for (int r = 0; r < 2; ++r)
+            pf[n >> 1][(n & 1) * 2 + r] =
+                r < kRowSets ? pack_f16(s[n][2 * r] * wmul[r % kRowSets], s[n][2 * r + 1] * wmul[r % kRowSets]) : 0u;
         // ---- O += P . V: per lane 16 (D = 128) or 8 dims of 8 tokens
         float unbias[2] = {0.f, 0.f};
         if constexpr (I8) {  // the sum of the rounded weights: a product with f16 ones
@@ -597,7 +608,6 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           unbias[0] = -128.f * kI8Unit * w1[0];
           unbias[1] = -128.f * kI8Unit * w1[2];
         }
-        const float vmul = I8 ? vref * (1.f / kI8Unit) : vref;
         constexpr int kWords = D / 32;  // words of a lane's run of dims
         uint32_t vw[4][2][kWords];      // [8-token group][token of the pair][word]
 #pragma unroll
@@ -644,7 +654,7 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
           for (int d = 0; d < 4; ++d)
 #pragma unroll
             for (int r = 0; r < kRowSets; ++r)
-              fma_pair(o[4 * q + d][2 * r], o[4 * q + d][2 * r + 1], c[d][2 * r], c[d][2 * r + 1], vmul);
+              fma_pair(o[4 * q + d][2 * r], o[4 * q + d][2 * r + 1], c[d][2 * r], c[d][2 * r + 1], vmul[r]);
         }
       }
       __syncwarp();

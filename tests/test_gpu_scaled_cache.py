@@ -330,3 +330,69 @@ def test_append_then_attend():
             rel = np.linalg.norm(o.cpu().numpy() - O) / np.linalg.norm(O)
             # e4m3 is off by 2^-4 of a value at most, int8 by half a 127th of its block's largest (about 4 sigma)
             assert rel < (2.0 ** -4 if cache == "e4m3" else 4 / 127), (cache, length, rel)
+
+
+def _check_visible(c, o, lse, causal, where=""):
+    """As _check, with every bound taken from the keys that the row itself sees.  A weight times its V scale, w, is
+    held in 11 bits (2^-11 of itself; a 2^-39th of the row's largest where it is less than a 2^-28th of that), the
+    divisor is the sum of the exact weights; int8 codes carry a bias of 128 whose sum over 32 tokens comes out again
+    in fp32 (34 additions of 2^-23 twice: 2^-10 of the sum of w, in units of one code)."""
+    q = c.q.double().cpu().numpy()
+    qmax, g, sm = (127.0 if c.cache == "i8" else 448.0), c.hq // c.hk, c.d ** -0.5
+    for r, L in enumerate(c.lengths):
+        k, v, t = c.values(0, r), c.values(1, r), np.arange(int(L))
+        page = c.kv_indices[c.kv_indptr[r] + t // c.page]
+        vs = c.scale[1][page, t % c.page // c.block].astype(np.float64)
+        n = int(c.qo_indptr[r + 1] - c.qo_indptr[r])
+        for i in range(n):
+            seen = int(L) - n + i + 1 if causal else int(L)
+            row = int(c.qo_indptr[r]) + i
+            for h in range(c.hq):
+                kk, vv, w = k[:seen, h // g], v[:seen, h // g], vs[:seen, h // g]
+                s = sm * (kk @ q[row, h])
+                M = sm * (np.abs(kk) @ np.abs(q[row, h])).max()
+                want = np.log(np.exp(s - s.max()).sum()) + s.max()
+                p = np.exp(s - want)
+                e = (c.d + 4) * 2.0 ** -23 * M + 2.0 ** -22 + seen * 2.0 ** -24
+                assert abs(float(lse[row, h]) - want) <= e + 2.0 ** -23 * abs(want), (where, r, i, h)
+                tol = (p @ np.abs(vv)) * (2.0 ** -11 + 2.0 ** -20 + 2 * e + seen * 2.0 ** -23)
+                tol = tol + seen * 2.0 ** -39 * (p * w).max() * qmax + (2.0 ** -10 * (p @ w) if c.cache == "i8" else 0.0)
+                if o.dtype == torch.bfloat16:
+                    tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(p @ vv)
+                err = np.abs(o[row, h].double().cpu().numpy() - p @ vv)
+                assert np.all(err <= tol), (where, r, i, h, float((err / np.maximum(tol, 1e-300)).max()))
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "i8"])
+@pytest.mark.parametrize("page,block", [(16, 16), (32, 8), (12, 4)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (16, 2, 128), (2, 2, 128)])
+def test_a_hidden_block_of_large_values_leaves_the_others_alone(cache, page, block, hq, hk, d):
+    """The last token begins a block whose V scale is 2^k of the others'.  The first query token does not see it, nor
+    may its result lose a bit to it."""
+    for k in (0, 12, 18, 22, 26, 40):
+        c = Case(31 + k, [2 * page + 1, 1 + block, 5 * page + 1], [2, 2, 2], hq, hk, d, page, block, cache, spread=0.3)
+        for r, n in enumerate(c.lengths):
+            at = int(n) - 1
+            c.scale[1][c.kv_indices[c.kv_indptr[r] + at // page], at % page // block] *= np.float32(2.0 ** k)
+        o, lse, _ = _run(c, True)
+        _check_visible(c, o, lse, True, where=k)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "i8"])
+@pytest.mark.parametrize("page,block", [(16, 16), (12, 4)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 64), (16, 1, 128)])
+def test_an_unattended_block_of_large_values_leaves_the_others_alone(cache, page, block, hq, hk, d):
+    """Every other block has a V scale 2^k of its neighbour's and scores that leave it a weight of 2^-2k."""
+    for k in (10, 18, 22, 26, 40):
+        c = Case(41 + k, [3 * page + 5], [1], hq, hk, d, page, block, cache, poison=False, spread=0.3)
+        small = np.zeros((c.num_pages, page // block), bool)
+        for t in range(0, int(c.lengths[0]), block):
+            small[c.kv_indices[t // page], t % page // block] = t // block % 2 == 0
+        c.q[:] = 1.0
+        c.code[0][:] = 64 if cache == "i8" else 0x38          # 64 and 1.0: all keys alike
+        unit = 64.0 if cache == "i8" else 1.0
+        c.scale[0][:] = 0.0                                    # large values: score 0
+        c.scale[0][small] = 2 * k * np.log(2.0) / (d ** 0.5 * unit)   # small ones: 2 k ln 2
+        c.scale[1][~small] *= np.float32(2.0 ** k)
+        o, lse, _ = _run(c, False)
+        _check_visible(c, o, lse, False, where=k)

@@ -107,6 +107,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// a += low half, b += high half, exact operands and one fp32 rounding each
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t h) {
+  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tadd.rn.f32.bf16 %0, x, %0;\n\tadd.rn.f32.bf16 %1, y, %1;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "r"(h));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -118,11 +124,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// One row of a tile: p = 2^(s * scale - m), bf16 pairs into the row's P columns, their sum into la.
+// One row of a tile: p = 2^(s * scale - m), bf16 pairs into the row's P columns, the sum of the exact p
+// into la and of the rounded ones into lb (as bf16 addends: 956 us on 4096 query tokens over 16384 keys, 32/8 heads;
+// widened and added in pairs 970; without them 920, 16 ragged prompts 204, 222 and 196).
 // (Two to four of every eight pairs by a polynomial on the FMA pipe measured slower: 1038 and 1118 us
 // against 1011; the warps are bound by instructions, not by the exponential unit.)
 __device__ __forceinline__ void weights(const float (&s)[kTile], uint64_t sc2, uint64_t nm2, uint32_t ts,
-                                        uint64_t (&la)[2]) {
+                                        uint64_t (&la)[2], float (&lb)[4]) {
 #pragma unroll
   for (int c = 0; c < kTile; c += 32) {
     float pw[16];
@@ -134,8 +142,10 @@ __device__ __forceinline__ void weights(const float (&s)[kTile], uint64_t sc2, u
       p0 = ex2(p0);
       p1 = ex2(p1);
       const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-      pw[e >> 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h2));
+      const uint32_t h = *reinterpret_cast<const uint32_t*>(&h2);
+      pw[e >> 1] = __uint_as_float(h);
       la[(e >> 1) & 1] = add2(la[(e >> 1) & 1], pk2(p0, p1));
+      add_bf16x2(lb[e & 2], lb[(e & 2) + 1], h);
     }
     tc::tmem_st_x16(ts + c / 2, pw);
   }
@@ -370,9 +380,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const PromptItem w = next;
       const Side s_me = side_of(w, x);
       const int tiles = s_me.tiles, all_tiles = max(tiles, side_of(w, 1 - x).tiles);
-      // l: sum of the exact weights, the divisor of O too: P V multiplies them rounded to bf16, each
-      // off by 2^-9 at most and to either side, as far as a bf16 O is from its own value
-      float m = -INFINITY, l = 0.f;
+      // P V multiplies the weights rounded to bf16, each off by 2^-9 of itself at most (half a step of a
+      // bf16 O).  l: sum of the exact weights, for the LSE; lr: of the rounded ones, O's divisor, so that keys
+      // of one value return it, and a row dominated by one key that key's V, whatever the weights' rounding
+      float m = -INFINITY, l = 0.f, lr = 0.f;
       const int64_t lim64 = w.causal ? min((int64_t)w.kv_len, (int64_t)s_me.limit + r) : (int64_t)w.kv_len;
       const int limit = (int)max(lim64, (int64_t)0);
       const int warp_limit = __shfl_sync(0xffffffffu, limit, 0);  // the warp's first row sees fewest
@@ -412,6 +423,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
           const float mn = raise ? mx : m;
           const float al = mn == m ? 1.f : ex2(m - mn);
           l *= al;
+          lr *= al;
           m = mn;
           if (j > 0) {  // a full S(j) means P V(j - 1) is done
 #pragma unroll 1
@@ -444,11 +456,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
         const float mm = m == -INFINITY ? 0.f : m;
         const uint64_t sc2 = pk2(a.scale_log2, a.scale_log2), nm2 = pk2(-mm, -mm);
         uint64_t la[2] = {0, 0};
-        weights(s, sc2, nm2, ts, la);
+        float lb[4] = {0.f, 0.f, 0.f, 0.f};
+        weights(s, sc2, nm2, ts, la, lb);
         {
           float a0, a1;
           upk2(add2(la[0], la[1]), a0, a1);
           l += a0 + a1;
+          lr += (lb[0] + lb[1]) + (lb[2] + lb[3]);
         }
         tc::tmem_wait_st();
         tc::tc_fence_before();
@@ -463,7 +477,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       }
       next = a.items[min(i + 1, i_end - 1)];  // on its way while the results are stored
       const bool some = l > 0.f || l != l;
-      const float inv = some ? 1.f / l : 0.f;
+      const float inv = some ? 1.f / lr : 0.f;
       const int rows = min(s_me.n, a.total_q - s_me.q0);
       const bool part = w.part_row >= 0;
       // this tile's first row, and rows a token apart

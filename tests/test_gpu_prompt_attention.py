@@ -325,3 +325,31 @@ def test_two_captured_steps_side_by_side():
         for o, w in zip(outs, want):
             for x, y in zip(o, w):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("hq,hk,d", [(4, 2, 128), (3, 3, 64), (1, 1, 128)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([300], [300]), ([40, 7], [260, 300])])
+def test_keys_of_one_value_return_it(hq, hk, d, q_lens, kv_lens):
+    """Every key of a KV head has the same V, and a few scores of a row within the 2^8 by which the running maximum may
+    lag outweigh the others: the weights' rounding, to 2^-9 each, has to come out again in the divisor.  What is
+    left is fp32: L products and additions in the numerator, L additions in the divisor (2^-24 each; twice that for the
+    tensor cores' sums), the reciprocal, its product and a merge."""
+    for seed, boost in ((22, 1.0), (23, 3.0), (24, 6.0)):
+        c = Case(seed, q_lens, kv_lens, hq, hk, d, boost=boost)
+        c.v[:] = c.v[:1].clone()
+        for causal in (True, False):
+            o, lse, _ = c.run(causal)
+            want = c.v[0].double().repeat_interleave(hq // hk, dim=0)[None]
+            tol = want.abs() * (3 * 300 + 8) * 2.0 ** -24
+            err = (o.double() - want).abs()
+            assert bool(torch.all(err <= tol)), (boost, causal, float((err / tol).max()))
+            c.check(o, lse, causal)
+
+
+def test_keys_of_one_value_over_cut_keys():
+    c = Case(25, [60], [6000], 4, 1, 128, boost=4.0)
+    c.v[:] = c.v[:1].clone()
+    o, lse, ex = c.run(True)
+    assert ex["plan"].info.max_splits > 1
+    want = c.v[0].double().expand(60, 4, 128)
+    assert bool(torch.all((o.double() - want).abs() <= want.abs() * (3 * 6000 + 16) * 2.0 ** -24))

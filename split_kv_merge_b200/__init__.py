@@ -342,6 +342,19 @@ def plan_mla(batch_q_len: int, kv_indptr, kv_last_page_len, page_size: int, num_
                  policy, split_page_start, "skv_plan_mla")
 
 
+def scaled_key(qo_indptr, kv_indptr, kv_last_page_len, causal, *shape) -> tuple:
+    """What a plan of plan_paged_scaled depends on: every request's query rows and pages, with ``causal`` its length
+    too (it sets the keys that query tokens see), page size, heads and head_dim."""
+    return (_i32(qo_indptr).tobytes(), _i32(kv_indptr).tobytes(), _i32(kv_last_page_len).tobytes() if causal else None,
+            bool(causal), *shape)
+
+
+def prompt_key(qo_indptr, kv_indptr, causal, *shape) -> tuple:
+    """What a plan of plan_prompt depends on: every sequence's query and key rows, ``causal``, heads and head_dim."""
+    qo = _i32(qo_indptr).tobytes()
+    return (qo, qo if kv_indptr is None else _i32(kv_indptr).tobytes(), bool(causal), *shape)
+
+
 def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, num_qo_heads: int, num_kv_heads: int,
                       head_dim: int, causal: bool = False, policy="balanced", param: int = 0,
                       split_page_start: Optional[Sequence[Sequence[int]]] = None) -> Plan:
@@ -351,7 +364,7 @@ def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, nu
     plan = _plan(_plan_scaled, lambda pol: (b, _ptr_i32(qo), _ptr_i32(ki), _ptr_i32(la), page_size, num_qo_heads,
                                             num_kv_heads, head_dim, int(causal), pol, param),
                  policy, split_page_start, "skv_plan_paged_scaled")
-    plan.made_for = (b, int(qo[-1]), int(ki[-1]), page_size, num_qo_heads, num_kv_heads, head_dim, bool(causal))
+    plan.made_for = scaled_key(qo, ki, la, causal, page_size, num_qo_heads, num_kv_heads, head_dim)
     return plan
 
 
@@ -370,9 +383,8 @@ def plan_prompt(qo_indptr, kv_indptr, num_qo_heads: int, num_kv_heads: int, head
         words = np.empty(info.plan_words, dtype=np.int32)
         code = _plan_prompt(*args, _ptr_i32(words), words.size, ctypes.byref(info))
     _check(code, "skv_plan_prompt")
-    total_kv = int(qo[-1] if ki is None else ki[-1])
     return Plan(words[: info.plan_words].copy(), info,
-                made_for=(len(qo) - 1, int(qo[-1]), total_kv, num_qo_heads, num_kv_heads, head_dim, bool(causal)))
+                made_for=prompt_key(qo, ki, causal, num_qo_heads, num_kv_heads, head_dim))
 
 
 # ----------------------------------------------------------------------------- launches

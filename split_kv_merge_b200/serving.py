@@ -11,7 +11,8 @@ from typing import Optional
 
 import numpy as np
 
-from . import BF16, F32, Plan, SkvError, _check, _ROPE, _ROPE_SCALING, _rope_frequencies, plan_paged_scaled, plan_prompt
+from . import (BF16, F32, Plan, SkvError, _check, _ROPE, _ROPE_SCALING, _rope_frequencies, plan_paged_scaled, plan_prompt,
+               prompt_key, scaled_key)
 
 _ext = None
 _O_CODE = {}
@@ -126,7 +127,7 @@ def _o_code(o_dtype) -> int:
 
 def _same(plan: Plan, made_for: tuple):
     if plan.made_for is not None and plan.made_for != made_for:
-        _bad(f"the plan was made for other requests: {plan.made_for}, not {made_for}")
+        _bad("the plan was made for other requests: their lengths, heads, page size and causal must be the call's")
 
 
 def _dev_i32(a, like):
@@ -143,8 +144,9 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
     bf16, caches [num_pages, P, Hk, D] float8_e4m3fn or int8, ``k_scale`` / ``v_scale`` float32
     [num_pages, P / block, Hk], as ``paged_kv_append`` writes them.  ``causal``: a request's query tokens are
     its last positions and each sees keys up to its own.  Host page-table shape arrays (``*_h``) feed
-    the planner; ``plan`` (``plan_paged_scaled`` of the same lengths, heads and ``causal``) and device copies
-    ``kv_indptr`` / ``kv_last_page_len`` may be kept over the layers of a step.
+    the planner; ``plan`` (``plan_paged_scaled`` of the same lengths, heads and ``causal``, which are compared; without
+    ``causal`` the last pages may have filled since) and device copies ``kv_indptr`` / ``kv_last_page_len`` may be
+    kept over the layers of a step.
     Returns (o, lse, extras) with extras = {"plan", "workspace"} (the split partials' buffer)."""
     if stream is not None:
         with _on_stream(stream, q):
@@ -160,8 +162,8 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
         plan = plan_paged_scaled(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, k_cache.shape[1], q.shape[1],
                                  k_cache.shape[2], q.shape[2], causal, policy, param, split_page_start)
     else:
-        _same(plan, (len(qo_indptr_h) - 1, int(qo_indptr_h[-1]), int(kv_indptr_h[-1]), k_cache.shape[1], q.shape[1],
-                     k_cache.shape[2], q.shape[2], bool(causal)))
+        _same(plan, scaled_key(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, causal, k_cache.shape[1], q.shape[1],
+                               k_cache.shape[2], q.shape[2]))
     if plan.device is None:
         plan.to(q.device)
     if kv_indptr is None:
@@ -181,8 +183,8 @@ def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = T
     """Attention over packed prompts (skv_prompt_attn_fwd): q [total_q, Hq, D], k, v [total_kv, Hk, D] bf16, any
     token / head strides; sequence r has query rows qo_indptr_h[r] .. and key rows kv_indptr_h[r] ..
     (default: the same rows).  ``causal``: its query tokens are its last positions.  ``plan``
-    (``plan_prompt`` of the same lengths, heads and ``causal``) may be kept over the layers of a step.  Rows of
-    outputs given as ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
+    (``plan_prompt`` of the same lengths, heads and ``causal``, which are compared) may be kept over the layers of
+    a step.  Rows of outputs given as ``o_out`` / ``lse_out`` behind the last sequence are left as they are.
     Returns (o, lse, extras) with extras = {"plan", "workspace"} (the partials' buffer)."""
     if stream is not None:
         with _on_stream(stream, q):
@@ -195,9 +197,7 @@ def prompt_attention(q, k, v, qo_indptr_h, kv_indptr_h=None, *, causal: bool = T
     if plan is None:
         plan = plan_prompt(qo_indptr_h, kv_indptr_h, q.shape[1], k.shape[1], q.shape[2], causal)
     else:
-        ki = qo_indptr_h if kv_indptr_h is None else kv_indptr_h
-        _same(plan, (len(qo_indptr_h) - 1, int(qo_indptr_h[-1]), int(ki[-1]), q.shape[1], k.shape[1], q.shape[2],
-                     bool(causal)))
+        _same(plan, prompt_key(qo_indptr_h, kv_indptr_h, causal, q.shape[1], k.shape[1], q.shape[2]))
     if plan.device is None:
         plan.to(q.device)
     o, lse, ws = ext.prompt_attention(q, k, v, plan.device, ctypes.addressof(plan.info), sm_scale, _o_code(o_dtype),

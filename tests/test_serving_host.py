@@ -421,3 +421,44 @@ def test_prompt_struct_layout():
         pytest.skip("needs a C compiler")
     got, want = c_layout([(skv.PromptParams, "skv_prompt_params")])
     assert got == want
+
+
+def test_a_kept_plan_is_compared_by_every_length():
+    """Equal totals are not equal requests: other borders between them, or another length in the last page."""
+    torch = pytest.importorskip("torch")
+    q, k = torch.zeros(9, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 2, 64, dtype=torch.bfloat16)
+    for made, qo, kv in ((([0, 4, 9], None), [0, 8, 9], None), (([0, 4, 9], [0, 4, 9]), [0, 4, 9], [0, 5, 9]),
+                         (([0, 4, 9], None), [0, 4, 9], [0, 8, 9])):
+        for causal in (True, False):
+            with pytest.raises(ValueError, match="plan was made for"):
+                skv.prompt_attention(q, k, k, qo, kv, causal=causal, plan=skv.plan_prompt(*made, 4, 2, 64, causal))
+    cache, scale = torch.zeros(3, 16, 2, 64, dtype=torch.int8), torch.zeros(3, 1, 2)
+    call = lambda plan, qo, ki, la, causal: skv.paged_attention_scaled(  # noqa: E731
+        q, cache, cache, scale, scale, qo, ki, None, la, causal=causal, plan=plan)
+    for made, now, causal in ((([0, 1, 3], [0, 1, 3], [5, 5]), ([0, 2, 3], [0, 1, 3], [5, 5]), False),
+                              (([0, 1, 2], [0, 1, 3], [5, 5]), ([0, 1, 2], [0, 2, 3], [5, 5]), False),
+                              (([0, 1, 2], [0, 1, 3], [5, 5]), ([0, 1, 2], [0, 1, 3], [5, 6]), True),
+                              (([0, 1, 2], [0, 1, 3], [6, 4]), ([0, 1, 2], [0, 1, 3], [5, 5]), True)):
+        with pytest.raises(ValueError, match="plan was made for"):
+            call(skv.plan_paged_scaled(*made, 16, 4, 2, 64, causal), *now, causal)
+
+
+def test_a_kept_plan_serves_equal_lengths_however_they_are_held():
+    """The comparison passes (these tensors are then refused for not being on a GPU)."""
+    torch = pytest.importorskip("torch")
+    q, k = torch.zeros(9, 4, 64, dtype=torch.bfloat16), torch.zeros(9, 2, 64, dtype=torch.bfloat16)
+    as_tensor = lambda a: torch.tensor(a)  # noqa: E731
+    plan = skv.plan_prompt([0, 4, 9], None, 4, 2, 64)
+    plan.device = torch.zeros(1, dtype=torch.int32)
+    for hold in (list, tuple, np.asarray, as_tensor):
+        for kv in (None, hold([0, 4, 9])):
+            with pytest.raises(ValueError, match="CUDA device"):
+                skv.prompt_attention(q, k, k, hold([0, 4, 9]), kv, plan=plan)
+    cache, scale = torch.zeros(3, 16, 2, 64, dtype=torch.int8), torch.zeros(3, 1, 2)
+    ids = torch.arange(3, dtype=torch.int32)
+    for causal, last in ((True, [5, 5]), (False, [5, 5]), (False, [5, 6])):   # not causal: the last page may fill
+        plan = skv.plan_paged_scaled([0, 1, 2], [0, 1, 3], [5, 5], 16, 4, 2, 64, causal)
+        plan.device = torch.zeros(1, dtype=torch.int32)
+        with pytest.raises(ValueError, match="CUDA device"):
+            skv.paged_attention_scaled(q, cache, cache, scale, scale, np.array([0, 1, 2]), [0, 1, 3], ids, last,
+                                       causal=causal, plan=plan)

@@ -433,10 +433,11 @@ SKV_API skv_status skv_mla_splice(const skv_splice_params* p, const skv_splice_c
  *   t <= L - n + i; a token that sees none gets O = 0, LSE = -inf.  Made for a few query tokens
  *   per request (decode, drafted tokens); every tile of 8 or 16 query rows (tokens x group)
  *   streams the request's keys again.
- *   Scales are >= 0; below 2^-126 they count as 0, and |q| * sm_scale * k_scale * 2^24 and
- *   v_scale * 2^24 must be finite.  A request has at most 2^30 tokens.  A key's weight times its V
- *   scale is rounded to 11 bits (to a 2^-39th of the row's largest among 32 neighbouring tokens where
- *   it is below a 2^-28th of that); keys that the row does not see have no part in that.
+ *   sm_scale is finite, of either sign.  Scales are >= 0; below 2^-126 they count as 0, and
+ *   |q| * sm_scale * k_scale * 2^24 and v_scale * 2^24 must be finite.  A request has at most 2^30
+ *   tokens.  A key's weight times its V scale is rounded to 11 bits (to a 2^-39th of the row's
+ *   largest among 32 neighbouring tokens where it is below a 2^-28th of that); keys that the row
+ *   does not see have no part in that.
  *   Slots past a request's length may hold anything, NaN codes and scales included.  A key that
  *   some query token of its request sees must have finite K, V and scales: where it is masked
  *   for another token of the request its weight is 0, and 0 x NaN is not 0.

@@ -627,6 +627,7 @@ skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* sp, const in
   if (p->kv_dtype != SKV_E4M3 && p->kv_dtype != SKV_I8) return SKV_ERR_UNSUPPORTED;
   if (p->o_dtype != SKV_F32 && p->o_dtype != SKV_BF16) return SKV_ERR_UNSUPPORTED;
   if (sp->block_tokens < 1 || p->page_size % sp->block_tokens != 0) return SKV_ERR_INVALID;
+  if (!std::isfinite(p->sm_scale)) return SKV_ERR_INVALID;  // the kernel's maxima would drop a NaN
   if (info->num_work == 0) return SKV_OK;  // no query rows: nothing to launch
   if (!p->q || !p->k_cache || !p->v_cache || !p->kv_indptr || !p->kv_indices || !p->kv_last_page_len || !p->o ||
       !sp->k_scale || !sp->v_scale)

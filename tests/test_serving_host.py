@@ -462,3 +462,9 @@ def test_a_kept_plan_serves_equal_lengths_however_they_are_held():
         with pytest.raises(ValueError, match="CUDA device"):
             skv.paged_attention_scaled(q, cache, cache, scale, scale, np.array([0, 1, 2]), [0, 1, 3], ids, last,
                                        causal=causal, plan=plan)
+
+
+@pytest.mark.parametrize("scale", [math.nan, math.inf, -math.inf])
+def test_scaled_fwd_refuses_a_softmax_scale_that_is_not_finite(scale):
+    _, _, info = _plan_scaled(qo=[0, 4, 8], policy=1, param=2)
+    assert skv._scaled_fwd(ctypes.byref(_scaled_params(sm_scale=scale)), PTR, ctypes.byref(info), None) == skv.ERR_INVALID

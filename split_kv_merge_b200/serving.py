@@ -164,6 +164,8 @@ def paged_attention_scaled(q, k_cache, v_cache, k_scale, v_scale, qo_indptr_h, k
     else:
         _same(plan, scaled_key(qo_indptr_h, kv_indptr_h, kv_last_page_len_h, causal, k_cache.shape[1], q.shape[1],
                                k_cache.shape[2], q.shape[2]))
+    if kv_indices is None or kv_indices.numel() < kv_indptr_h[-1]:
+        _bad("kv_indices must hold every page id that kv_indptr names")
     if plan.device is None:
         plan.to(q.device)
     if kv_indptr is None:

@@ -468,3 +468,18 @@ def test_a_kept_plan_serves_equal_lengths_however_they_are_held():
 def test_scaled_fwd_refuses_a_softmax_scale_that_is_not_finite(scale):
     _, _, info = _plan_scaled(qo=[0, 4, 8], policy=1, param=2)
     assert skv._scaled_fwd(ctypes.byref(_scaled_params(sm_scale=scale)), PTR, ctypes.byref(info), None) == skv.ERR_INVALID
+
+
+def test_scaled_attention_needs_every_page_id_that_the_table_names():
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    cache, scale = torch.zeros(4, 16, 2, 64, dtype=torch.int8), torch.zeros(4, 1, 2)
+    plan = skv.plan_paged_scaled([0, 1, 2], [0, 1, 3], [5, 5], 16, 4, 2, 64)
+    plan.device = torch.zeros(1, dtype=torch.int32)
+    for n, why in ((2, "kv_indices"), (0, "kv_indices"), (3, "CUDA device"), (4, "CUDA device")):
+        for kept in (plan, None):
+            with pytest.raises(ValueError, match=why):
+                skv.paged_attention_scaled(q, cache, cache, scale, scale, [0, 1, 2], [0, 1, 3],
+                                           torch.zeros(n, dtype=torch.int32), [5, 5], plan=kept)
+    with pytest.raises(ValueError, match="kv_indices"):
+        skv.paged_attention_scaled(q, cache, cache, scale, scale, [0, 1, 2], [0, 1, 3], None, [5, 5], plan=plan)

@@ -545,7 +545,8 @@ SKV_API skv_status skv_rope_frequencies(int32_t dim, double theta, int32_t scali
                                         double original_context, double low, double high, double* inv_freq_h,
                                         float* mscale);
 
-/* Arguments of skv_rope_apply.  x(token, head, d) = x[token*stride[0] + head*stride[1] + d]. */
+/* Arguments of skv_rope_apply.  x(token, head, d) = x[token*stride[0] + head*stride[1] + d].  Rows that are
+ * written lie apart: taken by size, each stride spans the dimensions before it. */
 typedef struct {
   const void* q;            /* [num_tokens, num_q_heads, head_dim] of dtype (num_q_heads 0: unused) */
   void* q_out;              /* may be q itself with the same strides (in place), else disjoint    */
@@ -590,10 +591,11 @@ SKV_API skv_status skv_rope_apply(const skv_rope_params* p, skv_stream_t stream)
  *   2^-126 gets scale 0 and new codes of zero.  A value that is not finite spoils at most its own block
  *   and head.
  *
- *   No page slot, and with block scales no block, may be written by two requests of a call; the
- *   cache, scales and outputs must not overlap the inputs.  Errors found on the device (a page
- *   id outside [0, num_pages): SKV_DEV_PAGE_OOB; a request shorter than its new tokens:
- *   SKV_DEV_PLAN_BAD) go to *status and skip the tokens concerned.
+ *   No page slot, and with block scales no block, may be written by two requests of a call, or twice
+ *   by one whose table names a page twice.  Rows of the caches, scales and q_out lie apart (taken by
+ *   size, each stride spans the dimensions before it), and none overlaps an input.  Errors found on
+ *   the device (a page id outside [0, num_pages): SKV_DEV_PAGE_OOB; a request shorter than its new
+ *   tokens: SKV_DEV_PLAN_BAD) go to *status and skip the tokens concerned.
  * ----------------------------------------------------------------------------------------- */
 typedef struct {
   const void* k;            /* bf16 [num_rows, Hk, D], (token, head) strides                        */

@@ -41,12 +41,32 @@ skv_status check_rows(const void* base, const int64_t* stride, int64_t size) {
   return SKV_OK;
 }
 
+// Whether the rows (`extent` values each) of a strided array lie apart: taken by size, every stride spans the
+// dimensions before it.
+template <int N>
+bool rows_apart(const int64_t (&count)[N], const int64_t* stride, int64_t extent) {
+  int64_t st[N], n[N];
+  int dims = 0;
+  for (int i = 0; i < N; ++i) {
+    if (count[i] <= 1) continue;  // its stride is never used
+    int at = dims++;
+    for (; at > 0 && st[at - 1] > stride[i]; --at) st[at] = st[at - 1], n[at] = n[at - 1];
+    st[at] = stride[i], n[at] = count[i];
+  }
+  __int128 span = extent;
+  for (int i = 0; i < dims; ++i) {
+    if (st[i] < span) return false;
+    span += (__int128)st[i] * (n[i] - 1);
+  }
+  return true;
+}
+
 // Output rows, which may also be the input with the same strides; each has a place of its own.
 skv_status check_out_rows(const void* out, const int64_t* out_stride, const void* in, const int64_t* in_stride,
-                          int64_t size, int64_t tokens, int64_t heads) {
+                          int64_t size, int64_t tokens, int64_t heads, int64_t head_dim) {
   const skv_status st = check_rows(out, out_stride, size);
   if (st != SKV_OK) return st;
-  if ((tokens > 1 && out_stride[0] == 0) || (heads > 1 && out_stride[1] == 0)) return SKV_ERR_INVALID;
+  if (!rows_apart<2>({tokens, heads}, out_stride, head_dim)) return SKV_ERR_INVALID;
   if (out == in && (out_stride[0] != in_stride[0] || out_stride[1] != in_stride[1])) return SKV_ERR_INVALID;
   return SKV_OK;
 }
@@ -107,13 +127,15 @@ skv_status skv_rope_apply(const skv_rope_params* p, skv_stream_t stream) {
   if (p->num_q_heads > 0) {
     st = check_rows(p->q, p->q_stride, size);
     if (st == SKV_OK)
-      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, size, p->num_tokens, p->num_q_heads);
+      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, size, p->num_tokens, p->num_q_heads,
+                          p->head_dim);
     if (st != SKV_OK) return st;
   }
   if (p->num_k_heads > 0) {
     st = check_rows(p->k, p->k_stride, size);
     if (st == SKV_OK)
-      st = check_out_rows(p->k_out, p->k_out_stride, p->k, p->k_stride, size, p->num_tokens, p->num_k_heads);
+      st = check_out_rows(p->k_out, p->k_out_stride, p->k, p->k_stride, size, p->num_tokens, p->num_k_heads,
+                          p->head_dim);
     if (st != SKV_OK) return st;
   }
   if (p->rope.dim > 0 && p->positions == nullptr) return SKV_ERR_INVALID;
@@ -151,17 +173,19 @@ skv_status skv_paged_kv_append(const skv_append_params* p, skv_stream_t stream) 
     if (p->k_stride[i] < 0 || p->v_stride[i] < 0) return SKV_ERR_INVALID;
     if (p->k_stride[i] * size % 16 != 0 || p->v_stride[i] * size % 16 != 0) return SKV_ERR_ALIGNMENT;
     if (scaled && (p->k_scale_stride[i] < 0 || p->v_scale_stride[i] < 0)) return SKV_ERR_INVALID;
-    // what is written has a place of its own
-    const int32_t entries[3] = {p->num_pages, p->page_size, p->num_kv_heads};
-    if (entries[i] > 1 && (p->k_stride[i] == 0 || p->v_stride[i] == 0)) return SKV_ERR_INVALID;
-    const int32_t scales[3] = {p->num_pages, scaled ? p->page_size / p->block_tokens : 0, p->num_kv_heads};
-    if (scaled && scales[i] > 1 && (p->k_scale_stride[i] == 0 || p->v_scale_stride[i] == 0)) return SKV_ERR_INVALID;
+  }
+  // what is written has a place of its own
+  const int64_t rows[3] = {p->num_pages, p->page_size, p->num_kv_heads};
+  if (!rows_apart(rows, p->k_stride, p->head_dim) || !rows_apart(rows, p->v_stride, p->head_dim)) return SKV_ERR_INVALID;
+  if (scaled) {
+    const int64_t scales[3] = {p->num_pages, p->page_size / p->block_tokens, p->num_kv_heads};
+    if (!rows_apart(scales, p->k_scale_stride, 1) || !rows_apart(scales, p->v_scale_stride, 1)) return SKV_ERR_INVALID;
   }
   if (!aligned16(p->k_cache) || !aligned16(p->v_cache)) return SKV_ERR_ALIGNMENT;
   if (p->num_q_heads > 0) {
     st = check_rows(p->q, p->q_stride, 2);
     if (st == SKV_OK)
-      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, 2, p->num_rows, p->num_q_heads);
+      st = check_out_rows(p->q_out, p->q_out_stride, p->q, p->q_stride, 2, p->num_rows, p->num_q_heads, p->head_dim);
     if (st != SKV_OK) return st;
   }
   return cuda_status(launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream)));

@@ -483,3 +483,33 @@ def test_scaled_attention_needs_every_page_id_that_the_table_names():
                                            torch.zeros(n, dtype=torch.int32), [5, 5], plan=kept)
     with pytest.raises(ValueError, match="kv_indices"):
         skv.paged_attention_scaled(q, cache, cache, scale, scale, [0, 1, 2], [0, 1, 3], None, [5, 5], plan=plan)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q_out_stride=(512, 56)), skv.ERR_INVALID),                            # heads of 64 values, 56 apart
+    (dict(q_out_stride=(448, 64)), skv.ERR_INVALID),                            # tokens of 8 x 64, 448 apart
+    (dict(q_out_stride=(64, 128)), skv.ERR_INVALID),                            # 3 tokens inside 2 heads' distance
+    (dict(k_out_stride=(120, 64)), skv.ERR_INVALID), (dict(k_out_stride=(1 << 62, 1 << 62)), skv.ERR_INVALID),
+])
+def test_rotated_rows_may_not_overlap(change, code):
+    assert skv._rope_apply(ctypes.byref(_rope_params(**change)), None) == code
+
+
+@pytest.mark.parametrize("change", [
+    dict(k_stride=(2048, 64, 64)), dict(k_stride=(1920, 128, 64)), dict(v_stride=(2048, 128, 48)),
+    dict(v_stride=(64, 1024, 512)), dict(q_out_stride=(496, 64)), dict(k_stride=(1 << 61, 1 << 61, 64)),
+    dict(kv_dtype=skv.I8, block_tokens=8, k_scale_stride=(3, 2, 1)),
+    dict(kv_dtype=skv.I8, block_tokens=8, v_scale_stride=(4, 1, 1)),
+    dict(kv_dtype=skv.E4M3, block_tokens=4, v_scale_stride=(2, 18, 3))])
+def test_appended_rows_and_scales_may_not_overlap(change):
+    assert skv._kv_append(ctypes.byref(_append_params(**change)), None) == skv.ERR_INVALID
+
+
+@pytest.mark.parametrize("change", [
+    dict(), dict(k_stride=(4096, 256, 128), v_stride=(4096, 256, 128)),         # K and V side by side
+    dict(k_stride=(2048, 64, 1024)), dict(k_stride=(64, 1152, 576)),            # heads, or pages, innermost
+    dict(kv_dtype=skv.I8, block_tokens=8, k_scale_stride=(8, 4, 2), v_scale_stride=(1, 18, 9))])
+def test_layouts_with_places_of_their_own_are_checked_on(change):
+    """These layouts pass: the call goes on to the next refusal (a misaligned q)."""
+    p = dict(dict(k_scale_stride=(4, 2, 1), v_scale_stride=(4, 2, 1)), **change)
+    assert skv._kv_append(ctypes.byref(_append_params(q=PTR + 2, **p)), None) == skv.ERR_ALIGNMENT

@@ -5,8 +5,8 @@
 Each .cu under csrc/ compiles to _build/<name>.o (skipped when newer than its sources and the
 headers), then everything links into split_kv_merge_b200/libsplitkv.so with the CUDA runtime
 linked statically.  csrc/binding.cpp becomes split_kv_merge_b200/_serving.so, the Python extension of
-the serving operators, against torch's libraries and libsplitkv.so.  The oracle is pure Python/numpy
-and needs no build step.
+the serving operators, against torch's libraries and libsplitkv.so (left out where torch is not
+installed).  The oracle is pure Python/numpy and needs no build step.
 """
 from __future__ import annotations
 
@@ -65,14 +65,15 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     return LIB
 
 
-def _binding(force: bool) -> str:
+def _binding(force: bool):
+    """The Python extension, made again when its source, the header, torch or the command line changed.  Without torch
+    there is none: the library is complete for C callers, and the serving calls say so when they are first used."""
     src = os.path.join(CSRC, "binding.cpp")
     inputs = [src, __file__, os.path.join(ROOT, "include", "splitkv.h")]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, inputs)):
-        return BINDING
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("the Python binding needs torch's headers")
+        print("torch not found: the Python extension of the serving operators was not built", file=sys.stderr)
+        return None
     torch = os.path.dirname(spec.origin)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", BINDING,
@@ -80,9 +81,19 @@ def _binding(force: bool) -> str:
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-L", PKG, "-lsplitkv", "-Wl,-rpath,$ORIGIN"]  # torch's own libraries are loaded before it
+    with open(os.path.join(torch, "version.py")) as f:
+        made_with = f"{cmd}\n{f.read()}"
+    stamp = os.path.join(BUILD, "serving.made_with")
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, inputs)):
+        if os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read() == made_with:
+                    return BINDING
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"binding failed:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_with)
     return BINDING
 
 

@@ -23,7 +23,11 @@ def _load():
     global _ext
     import torch
 
-    from . import _serving
+    try:
+        from . import _serving
+    except ImportError as e:
+        raise ImportError(f"the serving operators' extension is not there (run split_kv_merge_b200/build.py where torch "
+                          f"is installed): {e}") from e
     _O_CODE.update({None: F32, torch.float32: F32, torch.bfloat16: BF16})
     _serving.set_error(SkvError)
     _ext = _serving

@@ -94,6 +94,11 @@ int32_t rows(const at::Tensor& t, const char* name, at::ScalarType dtype, int64_
   return (int32_t)t.size(1);
 }
 
+// A tensor that a call has written: autograd refuses a backward pass that kept its old values.
+void written(const at::Tensor* t) {
+  if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // The tensors' device made current for a call (nothing to do when it is), and its stream.
 struct OnDevice {
   c10::cuda::OptionalCUDAGuard guard;
@@ -244,6 +249,8 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.rope = rope_of(rope_dim, a[5], a[4], f, a[7]);
     const skv_stream_t s = stream_of(dev);
     run("skv_rope_apply", [&] { return skv_rope_apply(&p, s); });
+    written(qo);
+    written(ko);
     return tuple(out(a[9], made[0]), out(a[10], made[1]));
   });
 }
@@ -317,7 +324,8 @@ PyObject* paged_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     std::memset(&p, 0, sizeof(p));
     const int32_t hk = rows(k, "k", at::kBFloat16, num, dim, dev, p.k_row_stride);
     const int32_t hv = rows(v, "v", at::kBFloat16, num, dim, dev, p.v_row_stride);
-    const Caches c = caches_of(tensor(a[2], "k_cache"), tensor(a[3], "v_cache"), dim, a[19], dev);
+    const at::Tensor &k_cache = tensor(a[2], "k_cache"), &v_cache = tensor(a[3], "v_cache");
+    const Caches c = caches_of(k_cache, v_cache, dim, a[19], dev);
     if (hk != c.hk || hv != c.hk) bad("k, v and the caches must have the same heads");
     p.k = k.data_ptr();
     p.v = v.data_ptr();
@@ -368,6 +376,11 @@ PyObject* paged_kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.status = const_cast<int32_t*>(optional_index(a[20], "status", -1, dev));
     const skv_stream_t s = stream_of(dev);
     run("skv_paged_kv_append", [&] { return skv_paged_kv_append(&p, s); });
+    written(&k_cache);
+    written(&v_cache);
+    written(kscale);
+    written(vscale);
+    written(qo);
     return out(a[12], made);
   });
 }
@@ -468,6 +481,8 @@ PyObject* paged_attention_scaled(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.kv_scale = 1.f;
     const skv_stream_t s = stream_of(dev);
     run("skv_paged_attn_scaled_fwd", [&] { return skv_paged_attn_scaled_fwd(&sp, plan, info, s); });
+    written(optional_tensor(a[12], "o_out"));
+    written(optional_tensor(a[13], "lse_out"));
     return tuple(out(a[12], r.o), out(a[13], r.lse), out(Py_None, ws));
   });
 }
@@ -503,6 +518,8 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.status = const_cast<int32_t*>(optional_index(a[9], "status", -1, dev));
     const skv_stream_t s = stream_of(dev);
     run("skv_prompt_attn_fwd", [&] { return skv_prompt_attn_fwd(&p, plan, info, s); });
+    written(optional_tensor(a[7], "o_out"));
+    written(optional_tensor(a[8], "lse_out"));
     return tuple(out(a[7], r.o), out(a[8], r.lse), out(Py_None, ws));
   });
 }

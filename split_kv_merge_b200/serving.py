@@ -3,7 +3,10 @@ over a block-scaled 8-bit cache and over packed prompts.
 
 The signatures and what they mean stand here; arguments are checked, outputs allocated and the C ABI
 called by the extension module built from ``csrc/binding.cpp``.  It needs torch and is loaded by the
-first call; planning and ``rope_frequencies`` do without."""
+first call; planning and ``rope_frequencies`` do without.
+
+The calls record nothing for autograd: their results have no history, whatever their inputs require.  Tensors
+that they write in place count as modified."""
 from __future__ import annotations
 
 import ctypes
@@ -89,7 +92,8 @@ def rope_apply(q, k, positions, *, rope_dim: Optional[int] = None, rope_theta: f
     or float32, any token / head strides), ``positions`` int32 [tokens] on the device.  The first
     ``rope_dim`` (default D) values of a head turn, the others are copied.  ``inv_freq`` (float64, host)
     replaces rope_theta^(-2p/rope_dim).  ``q_out=q`` / ``k_out=k`` rotates in place; ``inverse`` turns
-    back (and takes gradients through the rotation).  Returns (q_out, k_out)."""
+    back, and is the rotation's transpose for any ``mscale``: what the backward method of a caller's own
+    autograd function applies to the gradient.  Returns (q_out, k_out)."""
     if stream is not None:
         with _on_stream(stream, positions):
             return rope_apply(q, k, positions, rope_dim=rope_dim, rope_theta=rope_theta, rope_layout=rope_layout,

@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -165,7 +166,7 @@ PyObject* entry(Py_ssize_t given, Py_ssize_t wanted, Body body) {
   } catch (const Bad& e) {
     PyErr_SetString(PyExc_ValueError, e.what.c_str());
   } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    PyErr_SetString(THPException_OutOfMemoryError, e.what_without_backtrace());
   } catch (const c10::Error& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {

@@ -80,3 +80,11 @@ def test_no_history_and_the_gradient_by_the_inverse():
     # fp32 cos, sin, products and their sum: 2^-21 of the pair's |a| + |b|
     size = torch.cat([(w[..., 0:32:2].abs() + w[..., 1:32:2].abs()).repeat_interleave(2, -1) * 1.5, w[..., 32:].abs()], -1)
     assert bool(torch.all((x.grad.double() - z.grad).abs() <= size.double() * 2.0 ** -21))
+
+
+def test_running_out_of_memory_is_torchs_error():
+    """An output of 8.7 TB: torch's allocator refuses it, and nothing is launched."""
+    tokens = 1 << 20
+    x = torch.zeros(1, 1, 64, device=DEV, dtype=torch.bfloat16).expand(tokens, 65000, 64)
+    with pytest.raises(torch.OutOfMemoryError):
+        skv.rope_apply(x, None, torch.zeros(tokens, dtype=torch.int32, device=DEV))

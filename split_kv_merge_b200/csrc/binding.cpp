@@ -165,12 +165,8 @@ PyObject* entry(Py_ssize_t given, Py_ssize_t wanted, Body body) {
   } catch (const Raised&) {
   } catch (const Bad& e) {
     PyErr_SetString(PyExc_ValueError, e.what.c_str());
-  } catch (const c10::OutOfMemoryError& e) {
-    PyErr_SetString(THPException_OutOfMemoryError, e.what_without_backtrace());
-  } catch (const c10::Error& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own errors under torch's own names
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }

@@ -62,6 +62,12 @@ double real(PyObject* o) {
   return v;
 }
 
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v;
+}
+
 int cuda_index(const at::Tensor& t) {
   if (!t.is_cuda()) bad("tensors must be on a CUDA device");
   return t.get_device();
@@ -240,7 +246,7 @@ PyObject* rope_apply(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.num_k_heads = heads[1];
     p.head_dim = (int32_t)dim;
     p.dtype = dtype == at::kFloat ? SKV_F32 : SKV_BF16;
-    p.inverse = PyObject_IsTrue(a[8]);
+    p.inverse = truth(a[8]);
     const int32_t rope_dim = a[3] == Py_None ? (int32_t)dim : int32(a[3]);
     const Frequencies f(a[6], rope_dim);
     p.rope = rope_of(rope_dim, a[5], a[4], f, a[7]);

@@ -88,3 +88,9 @@ def test_running_out_of_memory_is_torchs_error():
     x = torch.zeros(1, 1, 64, device=DEV, dtype=torch.bfloat16).expand(tokens, 65000, 64)
     with pytest.raises(torch.OutOfMemoryError):
         skv.rope_apply(x, None, torch.zeros(tokens, dtype=torch.int32, device=DEV))
+
+
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    x = torch.zeros(2, 1, 64, device=DEV)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        skv.rope_apply(x, None, _i32([0, 1]), inverse=torch.zeros(2))

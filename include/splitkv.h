@@ -587,9 +587,13 @@ SKV_API skv_status skv_rope_apply(const skv_rope_params* p, skv_stream_t stream)
  *   amax over the new rows of the head in the block.  When the block's first slot is among the new
  *   ones, its old scale counts as 0 and its other codes stay as they are; otherwise, where the
  *   scale grew, the codes of the block's other slots are written again as
- *   rn(code * scale / scale'), so that they keep their values.  A block whose scale' is below
- *   2^-126 gets scale 0 and new codes of zero.  A value that is not finite spoils at most its own block
- *   and head.
+ *   rn(code * scale / scale'), which keeps their values to half a step of the new scale.  These
+ *   roundings add up: a token is rounded once when it is appended and once for each later call that
+ *   raises its block's scale, block_tokens - 1 of them at most (none in a block filled by one call).
+ *   With int8 its error stays within half the sum of the scales that it was held at; with e4m3 each
+ *   rounding moves it by 2^-4 of itself at most (half a subnormal step near zero).  A block whose
+ *   scale' is below 2^-126 gets scale 0 and new codes of zero.  A value that is not finite spoils at
+ *   most its own block and head.
  *
  *   No page slot, and with block scales no block, may be written by two requests of a call, or twice
  *   by one whose table names a page twice.  Rows of the caches, scales and q_out lie apart (taken by

@@ -422,3 +422,37 @@ def test_rows_past_32_bit_offsets():
         assert torch.equal(a, b)
     skv.rope_apply(spread, None, pos, q_out=spread)
     assert torch.equal(spread, want)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "i8"])
+@pytest.mark.parametrize("growth", [1.0, 1.07, 1.5])
+def test_a_block_filled_token_by_token_against_its_tokens(cache, growth):
+    """Each token `growth` times the last: a token's error is the sum of one rounding for every scale that it was held
+    at (int8: half of it; e4m3: 2^-4 of the value as it then was, or half the subnormal step 2^-9 of the scale).  The
+    scale is amax / qmax to 2^-22, each product of a re-encoding to 2^-24."""
+    n, hk, d, page = 32, 2, 64, 32
+    rng = np.random.default_rng(23)
+    x = [torch.from_numpy((rng.standard_normal((n, hk, d)) * growth ** np.arange(n)[:, None, None]).astype(np.float32))
+         .to(torch.bfloat16).to(DEV) for _ in range(2)]
+    codes = [torch.zeros(1, page, hk, d, dtype=CODE[cache], device=DEV) for _ in range(2)]
+    scales = [torch.zeros(1, 1, hk, device=DEV) for _ in range(2)]
+    want, bound, held = [_f64(t) for t in x], [np.zeros((n, hk, d)) for _ in x], [np.zeros(hk) for _ in x]
+    raised = 0
+    for t in range(n):
+        skv.paged_kv_append(x[0][t:t + 1], x[1][t:t + 1], *codes, _i32([0, 1]), _i32([0, 1]), _i32([0]), _i32([t + 1]),
+                            k_scale=scales[0], v_scale=scales[1])
+        for i in range(2):
+            s = _f64(scales[i])[0, 0]
+            grew = s > held[i]
+            raised += int(grew.sum()) if t else 0
+            live = np.zeros((n, hk, 1), bool)
+            live[t], live[:t] = True, grew[:, None]
+            step = 0.5 * s[:, None] if cache == "i8" else np.maximum(2.0 ** -4 * (np.abs(want[i]) + bound[i]), 2.0 ** -10 * s[:, None])
+            noise = 2.0 ** -21 * (np.abs(want[i]) + bound[i])
+            bound[i] += np.where(live, np.broadcast_to(step, bound[i].shape) + noise, 0.0)
+            held[i] = s
+            got = OS.decode(codes[i].view(torch.uint8).cpu().numpy()[0], cache) * s[:, None]
+            err = np.abs(got[:t + 1] - want[i][:t + 1])
+            assert np.all(err <= bound[i][:t + 1]), (t, i, float((err / bound[i][:t + 1]).max()))
+    top = [np.maximum.accumulate(np.abs(w).max(axis=2), axis=0) for w in want]
+    assert raised == sum(int((m[1:] > m[:-1]).sum()) for m in top) > 0       # a scale grows with its block's largest value

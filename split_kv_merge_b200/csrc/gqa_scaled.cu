@@ -187,6 +187,13 @@ __device__ __forceinline__ void fma_pair(float& o0, float& o1, float c0, float c
       : "+f"(o0), "+f"(o1)
       : "f"(c0), "f"(c1), "f"(f));
 }
+// (a, b) *= (fa, fb) in one packed instruction
+__device__ __forceinline__ void mul_pair(float& a, float& b, float fa, float fb) {
+  asm("{\n\t.reg .b64 x, f;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmul.rn.f32x2 x, x, f;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(fa), "f"(fb));
+}
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -584,8 +591,9 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             const float p0 = ex2f(fmaf(s[n][2 * r], f[r][n][0], nm));
             const float p1 = ex2f(fmaf(s[n][2 * r + 1], f[r][n][kTokScales - 1], nm));
             l[r] += p0 + p1;
-            s[n][2 * r] = p0 * vsc[n][0];
-            s[n][2 * r + 1] = p1 * vsc[n][kTokScales - 1];
+            s[n][2 * r] = p0;
+            s[n][2 * r + 1] = p1;
+            mul_pair(s[n][2 * r], s[n][2 * r + 1], vsc[n][0], vsc[n][kTokScales - 1]);
             wmax[r] = fmaxf(wmax[r], fmaxf(s[n][2 * r], s[n][2 * r + 1]));
           }
           wmax[r] = quad_max(wmax[r]);
@@ -596,9 +604,10 @@ gqa_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            pf[n >> 1][(n & 1) * 2 + r] =
-                r < kRowSets ? pack_f16(s[n][2 * r] * wmul[r % kRowSets], s[n][2 * r + 1] * wmul[r % kRowSets]) : 0u;
+          for (int r = 0; r < 2; ++r) {
+            if (r < kRowSets) mul_pair(s[n][2 * r], s[n][2 * r + 1], wmul[r % kRowSets], wmul[r % kRowSets]);
+            pf[n >> 1][(n & 1) * 2 + r] = r < kRowSets ? pack_f16(s[n][2 * r], s[n][2 * r + 1]) : 0u;
+          }
         // ---- O += P . V: per lane 16 (D = 128) or 8 dims of 8 tokens
         float unbias[2] = {0.f, 0.f};
         if constexpr (I8) {  // the sum of the rounded weights: a product with f16 ones

@@ -342,21 +342,17 @@ def plan_mla(batch_q_len: int, kv_indptr, kv_last_page_len, page_size: int, num_
                  policy, split_page_start, "skv_plan_mla")
 
 
-def _i32_bytes(a) -> bytes:
-    return a.tobytes() if type(a) is np.ndarray and a.dtype == np.int32 else _i32(a).tobytes()
-
-
 def scaled_key(qo_indptr, kv_indptr, kv_last_page_len, causal, *shape) -> tuple:
     """What a plan of plan_paged_scaled depends on: every request's query rows and pages, with ``causal`` its length
     too (it sets the keys that query tokens see), page size, heads and head_dim."""
-    return (_i32_bytes(qo_indptr), _i32_bytes(kv_indptr), _i32_bytes(kv_last_page_len) if causal else None, bool(causal),
-            *shape)
+    return (_i32(qo_indptr).tobytes(), _i32(kv_indptr).tobytes(), _i32(kv_last_page_len).tobytes() if causal else None,
+            bool(causal), *shape)
 
 
 def prompt_key(qo_indptr, kv_indptr, causal, *shape) -> tuple:
     """What a plan of plan_prompt depends on: every sequence's query and key rows, ``causal``, heads and head_dim."""
-    qo = _i32_bytes(qo_indptr)
-    return (qo, qo if kv_indptr is None else _i32_bytes(kv_indptr), bool(causal), *shape)
+    qo = _i32(qo_indptr).tobytes()
+    return (qo, qo if kv_indptr is None else _i32(kv_indptr).tobytes(), bool(causal), *shape)
 
 
 def plan_paged_scaled(qo_indptr, kv_indptr, kv_last_page_len, page_size: int, num_qo_heads: int, num_kv_heads: int,

@@ -476,6 +476,8 @@ SKV_API skv_status skv_paged_attn_scaled_fwd(const skv_paged_scaled_params* p, c
  *   Keys of other sequences never reach a result, NaN or not; a key that some query token of its
  *   own sequence sees must have finite K and V (where it is masked for another token its weight is
  *   0, and 0 x NaN is not 0).
+ *   Softmax weights are rounded to bf16 for the product with V, and O is divided by the sum of the
+ *   rounded ones; the LSE takes the exact ones.
  *   `num_sms` (0: the current device's) is what the plan balances over; sequences with few query
  *   tokens over many keys, and a few others where whole ones would leave SMs idle, are cut along the
  *   keys, their partials go to o_part / lse_part

@@ -14,8 +14,9 @@
 //     page size divides the tile or is a multiple of it, is a multiple of 8, and blocks are whole
 //     groups of 8 tokens (one scale per group and head is staged);
 //   - else by cp.async from four warps (any page size, block size and 16-byte strides; one scale per
-//     token and head).  Measured on the 64-request 64/8-head e4m3 decode, pages of 16: 225 us
-//     against 102 us by TMA (6.3 TB/s): address arithmetic for 4096 copies a stage holds the ring back.
+//     token and head).  64-request 64/8-head e4m3 decode: 209 us with blocks of 4 in pages of 16, 212
+//     with pages of 1, 272 with pages of 12, against 103 by TMA (pages and blocks of 16, 6.2 TB/s):
+//     address arithmetic for 4096 copies a stage holds the ring back.
 // With several query tokens the consumers bind it: 4 tokens over 171 k int8 tokens in pages of 64, 32/8
 // heads: 76 us (4.6 TB/s), issue slots 46 % busy, most of it widening and the softmax of 16 rows.
 //

@@ -17,12 +17,13 @@
 // shapes holds its issuer about 80 cycles (it runs for 64), a wait or commit after one some 200, and
 // one issuer for both sides was busy 4130 cycles per pair of tiles (clock stamps of one CTA).  The two
 // issue in strict turns: left to themselves A and B fall into step, both in the softmax and then both
-// at the tensor cores (1214 us against 956 us on 4096 query tokens over 16384 keys, 32/8 heads).
+// at the tensor cores (1214 us against 976 for that form, 4096 query tokens over 16384 keys, 32/8 heads).
 // What is left is the chain of one side: 2100 cycles of softmax, its weights' way to the issuer, 1024 of
 // MMAs, their scores' way back: 3800 for a pair of tiles, 2048 of them the tensor cores'.  Scores in two
-// buffers of 64 keys, which break that chain, measured slower (1072 us): a 128 x 64 x 16 product of two
+// buffers of 64 keys, which break that chain, measured slower (1072 us on 951): a 128 x 64 x 16 product of two
 // shared-memory operands takes 59 cycles, the one of 128 x 128 x 16 only 64.  Weights handed over in
-// halves with the maximum taken beside the exponentials: 1005 us.
+// halves with the maximum taken beside the exponentials: 1005 us.  (These cycles are from before the sum of
+// the rounded weights, which adds 4 % to the kernel: 920 -> 956 us.)
 // The running maximum is raised only when a score passes it by 2^8, so O is rarely rescaled.
 //
 // Persistent: the planner hands every CTA a list of items (a pair of query tiles and a range of
@@ -30,7 +31,7 @@
 // those that would make no full round, are cut along the keys into fp32 partials that the merge pass
 // joins.  An item's end costs about 5000 cycles (the last P V, its results, the next item's first
 // scores): its code runs once in a while and is kept short, and results leave by whole sectors (16
-// sequences of 64 .. 2048 tokens: 194 us, 204 with 16-byte stores, 218 with all of it unrolled).
+// sequences of 64 .. 2048 tokens: 194 us, 204 with 16-byte stores, 218 with all of it unrolled; now 203).
 // Roles: warps 0-3 softmax of A, 4-7 of B, warp 8 TMA (ring of K and V tiles in the order of use),
 // warps 9 and 10 the MMAs of A and of B.
 // All waits are bounded.
@@ -380,8 +381,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_consta
       const PromptItem w = next;
       const Side s_me = side_of(w, x);
       const int tiles = s_me.tiles, all_tiles = max(tiles, side_of(w, 1 - x).tiles);
-      // P V multiplies the weights rounded to bf16, each off by 2^-9 of itself at most (half a step of a
-      // bf16 O).  l: sum of the exact weights, for the LSE; lr: of the rounded ones, O's divisor, so that keys
+      // P V multiplies the weights rounded to bf16, each off by 2^-8 of itself at most (half a step, as a
+      // bf16 O is from its own value).  l: sum of the exact weights, for the LSE; lr: of the rounded ones, O's divisor, so that keys
       // of one value return it, and a row dominated by one key that key's V, whatever the weights' rounding
       float m = -INFINITY, l = 0.f, lr = 0.f;
       const int64_t lim64 = w.causal ? min((int64_t)w.kv_len, (int64_t)s_me.limit + r) : (int64_t)w.kv_len;

@@ -331,7 +331,7 @@ def test_two_captured_steps_side_by_side():
 @pytest.mark.parametrize("q_lens,kv_lens", [([300], [300]), ([40, 7], [260, 300])])
 def test_keys_of_one_value_return_it(hq, hk, d, q_lens, kv_lens):
     """Every key of a KV head has the same V, and a few scores of a row within the 2^8 by which the running maximum may
-    lag outweigh the others: the weights' rounding, to 2^-9 each, has to come out again in the divisor.  What is
+    lag outweigh the others: the weights' rounding, to 2^-8 each, has to come out again in the divisor.  What is
     left is fp32: L products and additions in the numerator, L additions in the divisor (2^-24 each; twice that for the
     tensor cores' sums), the reciprocal, its product and a merge."""
     for seed, boost in ((22, 1.0), (23, 3.0), (24, 6.0)):

@@ -396,3 +396,21 @@ def test_an_unattended_block_of_large_values_leaves_the_others_alone(cache, page
         c.scale[1][~small] *= np.float32(2.0 ** k)
         o, lse, _ = _run(c, False)
         _check_visible(c, o, lse, False, where=k)
+
+
+@pytest.mark.parametrize("policy,param", [("none", 0), ("balanced", 0)])
+def test_a_plan_without_causal_serves_last_pages_that_fill(policy, param):
+    c = Case(51, [700, 35, 1201], [1, 2, 1], 16, 4, 128, 16, 16, "i8", poison=False)
+    plan = skv.plan_paged_scaled(c.qo_indptr, c.kv_indptr, c.last, 16, 16, 4, 128, False, policy, param)
+    for step in range(3):                      # last pages of 12, 3 and 1 tokens, then of two more each
+        o, lse, _ = _run(c, False, plan=plan)
+        _check_visible(c, o, lse, False, where=step)
+        fresh = _run(c, False, policy=policy, param=param)
+        assert torch.equal(o, fresh[0]) and torch.equal(lse, fresh[1])
+        c.last, c.lengths = c.last + 2, c.lengths + 2
+    c.last, c.lengths = c.last - 4, c.lengths - 4
+    plan = skv.plan_paged_scaled(c.qo_indptr, c.kv_indptr, c.last, 16, 16, 4, 128, True, policy, param)
+    _run(c, True, plan=plan)
+    c.last = c.last + 1
+    with pytest.raises(ValueError, match="plan was made for"):
+        _run(c, True, plan=plan)
